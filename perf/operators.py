@@ -9,9 +9,10 @@ through a block table.  Four operators work on such a pool, held in bfloat16 or 
   read back;
 - "copy": whole pages copied inside the pools of all layers, as a forked sequence or a shrunk pool needs it.
 
-A 4-bit page of one KV head holds, for K and for V: 32 rows of D / 2 bytes of e2m1 codes (the even element in
-the low nibble), then 32 x D / 16 e4m3 block scales (K: [32][D / 16], V: [D / 16][32]), then 32 float32 row
-scales.  A row is quantised in float32 steps: s = amax / 2688 (0 for a row of zeros), b = e4m3(min(amax of 16 /
+A 4-bit page of one KV head holds 32 rows: 32 D / 2 bytes of e2m1 codes, then 32 D / 16 e4m3 block scales, then
+32 float32 row scales.  K: codes [32][D / 2] (the even element in the low nibble), block scales [32][D / 16].
+V, with position 8 t + 2 j + i of the page: codes [j][D / 16][t][16 elements] (position i = 0 in the low nibble,
+i = 1 in the high one), block scales [D / 16][32].  A row is quantised in float32 steps: s = amax / 2688 (0 for a row of zeros), b = e4m3(min(amax of 16 /
 (6 s), 448)), code = e2m1(clamp(x / (b s), -6, 6)) with ties to the even code; its value is e2m1 * b * s.
 """
 import math
@@ -169,7 +170,7 @@ def work(case):
 
 # ---------------------------------------------------------------- the pool's 4-bit form
 def _quantise(x):
-    """float32 rows [..., D] -> codes [..., D / 2], block scales [..., D / 16] (both bytes), row scales [...]."""
+    """float32 rows [..., D] -> e2m1 codes [..., D], block scales [..., D / 16] (both bytes), row scales [...]."""
     c = lambda v: torch.full((), v, device=x.device)  # a tensor: a division by a number becomes a product
     b16 = x.unflatten(-1, (-1, 16))
     amax = x.abs().amax(-1)
@@ -182,23 +183,39 @@ def _quantise(x):
     code = ((a > 0.25).to(torch.uint8) + (a >= 0.75).to(torch.uint8) + (a > 1.25).to(torch.uint8)
             + (a >= 1.75).to(torch.uint8) + (a > 2.5).to(torch.uint8) + (a >= 3.5).to(torch.uint8)
             + (a > 5.0).to(torch.uint8) + ((r < 0).to(torch.uint8) << 3))
-    return code[..., 0::2] | (code[..., 1::2] << 4), b.view(torch.uint8), s
+    return code, b.view(torch.uint8), s
 
 
 def _split_page(pool, case, v):
-    """Views of a 4-bit pool [pages][Hkv][bytes]: codes [.., 32, D / 2], block scales [.., 32, D / 16], row scales."""
+    """Views of a 4-bit pool [..][bytes]: packed codes (K [.., 32, D / 2], V [.., 4, D / 16, 4, 16]), block scales
+    [.., 32, D / 16] and row scales [.., 32]."""
     d = case["dim"]
-    codes = pool[..., :PAGE * d // 2].unflatten(-1, (PAGE, d // 2))
+    codes = pool[..., :PAGE * d // 2].unflatten(-1, (4, d // 16, 4, 16) if v else (PAGE, d // 2))
     scales = pool[..., PAGE * d // 2:PAGE * (d // 2 + d // 16)]
     scales = scales.unflatten(-1, (d // 16, PAGE)).transpose(-1, -2) if v else scales.unflatten(-1, (PAGE, d // 16))
     return codes, scales, pool.view(torch.float32)[..., PAGE * (d // 2 + d // 16) // 4:]
 
 
-def _values(codes, scales, s):
+def _pack(code, v):
+    """Codes of whole pages [.., 32, D] as the pages hold them."""
+    if not v:
+        return code[..., 0::2] | (code[..., 1::2] << 4)
+    c = code.unflatten(-2, (4, 4, 2)).unflatten(-1, (-1, 16))  # [.., t, j, i, D / 16, 16]
+    return (c[..., 0, :, :] | (c[..., 1, :, :] << 4)).movedim(-4, -2)
+
+
+def _unpack(codes, v):
+    """Codes [.., 32, D] of whole pages."""
+    both = torch.stack((codes & 15, codes >> 4), -1)
+    if not v:
+        return both.flatten(-2)
+    return both.movedim(-3, -5).movedim(-1, -3).flatten(-5, -3).flatten(-2)  # [.., t, j, i, D / 16, 16]
+
+
+def _values(code, scales, s):
     """float32 values of quantised rows."""
-    table = torch.tensor(E2M1 + tuple(-e for e in E2M1), device=codes.device)
-    both = torch.stack((table.repeat(16), table.repeat_interleave(16)), -1)  # a byte's two elements
-    x = both[codes.int()].flatten(-2).unflatten(-1, (-1, 16))
+    table = torch.tensor(E2M1 + tuple(-e for e in E2M1), device=code.device)
+    x = table[code.int()].unflatten(-1, (-1, 16))
     return ((x * scales.view(torch.float8_e4m3fn).float().unsqueeze(-1)).flatten(-2)) * s.unsqueeze(-1)
 
 
@@ -208,7 +225,7 @@ def _whole(pool, case, v, table):
     if case["fmt"] == BF16:
         return pages.flatten(2, 3).float()
     codes, scales, s = _split_page(pages, case, v)
-    return _values(codes, scales.contiguous(), s).flatten(2, 3)
+    return _values(_unpack(codes, v), scales.contiguous(), s).flatten(2, 3)
 
 
 # ---------------------------------------------------------------- inputs
@@ -217,8 +234,8 @@ def _store(pool, case, v, lo, x):
     if case["fmt"] == BF16:
         pool[lo:lo + x.shape[0]] = x.to(torch.bfloat16)
     else:
-        parts = _split_page(pool[lo:lo + x.shape[0]], case, v)
-        for p, y in zip(parts, _quantise(x)):
+        code, b, s = _quantise(x)
+        for p, y in zip(_split_page(pool[lo:lo + x.shape[0]], case, v), (_pack(code, v), b, s)):
             p.copy_(y)
 
 
@@ -319,9 +336,19 @@ def _plain_append(st):
             pool[page, :, slot] = x.to(torch.bfloat16)
             return pool[page, :, slot].float()
         codes, scales, s = _split_page(pool, case, v)
-        for p, y in zip((codes, scales, s), _quantise(x.float())):
-            p[page, :, slot] = y
-        return _values(codes[page, :, slot], scales[page, :, slot], s[page, :, slot])
+        code, scales[page, :, slot], s[page, :, slot] = _quantise(x.float())
+        if v:  # a byte holds two positions: what each nibble changes by is added to it
+            t, j, shift = slot // 8, slot // 2 % 4, (slot % 2 * 4).to(torch.uint8)[:, None, None, None]
+            at = codes[page, :, j, :, t] >> shift & 15
+            h, g, e = (torch.arange(n, device="cuda") for n in (codes.shape[1], codes.shape[3], 16))
+            of = lambda x: x[:, None, None, None]
+            codes.index_put_((of(page), h[:, None, None], of(j), g[:, None], of(t), e),
+                             (code.unflatten(-1, (-1, 16)) - at) << shift, accumulate=True)
+            code = (codes[page, :, j, :, t] >> shift & 15).flatten(-2)
+        else:
+            codes[page, :, slot] = code[..., 0::2] | (code[..., 1::2] << 4)
+            code = torch.stack((codes[page, :, slot] & 15, codes[page, :, slot] >> 4), -1).flatten(-2)
+        return _values(code, scales[page, :, slot], s[page, :, slot])
 
     return one(st["K"], st["k"], False), one(st["V"], st["v"], True)
 
@@ -369,8 +396,13 @@ def _exact_page_values(st, which, i, n):
     pages = st[which][st["table"][i, :(n + PAGE - 1) // PAGE].long()]
     if case["fmt"] == BF16:
         return pages.double().permute(0, 2, 1, 3).reshape(-1, hk, d)[:n]
-    raw = pages.permute(0, 1, 2).long()
-    nib = torch.stack((raw[..., :16 * d] % 16, raw[..., :16 * d] // 16), -1).reshape(-1, hk, PAGE, d)
+    raw = pages.long()
+    if which == "K":
+        nib = torch.stack((raw[..., :16 * d] % 16, raw[..., :16 * d] // 16), -1).reshape(-1, hk, PAGE, d)
+    else:
+        pos, dim = torch.meshgrid(torch.arange(PAGE), torch.arange(d), indexing="ij")
+        byte = ((pos // 2 % 4 * (d // 16) + dim // 16) * 4 + pos // 8) * 16 + dim % 16
+        nib = (raw[..., byte.cuda()] // 16 ** (pos % 2).cuda()) % 16
     mag = nib % 8
     e, m = mag // 2, mag % 2
     x = torch.where(e == 0, m * 0.5, (1 + 0.5 * m.double()) * 2.0 ** (e - 1).double()) * (1 - 2 * (nib // 8)).double()
