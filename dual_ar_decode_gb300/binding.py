@@ -13,7 +13,9 @@ TF_OK = 0
 STATUS = {0: "TF_OK", 1: "TF_E_INVAL", 2: "TF_E_NOMEM", 3: "TF_E_CUDA", 4: "TF_E_STATE",
           5: "TF_E_CAPACITY", 6: "TF_E_TIMEOUT", 7: "TF_E_NUMERIC"}
 TF_WEIGHT_BF16, TF_WEIGHT_FP8, TF_WEIGHT_NVFP4 = 0, 1, 2
-TF_DTYPE_BF16, TF_DTYPE_FP8_E4M3, TF_DTYPE_NVFP4 = 0, 1, 2
+TF_DTYPE_BF16, TF_DTYPE_FP8_E4M3, TF_DTYPE_NVFP4, TF_DTYPE_F32 = 0, 1, 2, 3
+TF_KV_BF16, TF_KV_NVFP4 = 0, 1
+TF_CACHE_BAD_PAGE, TF_CACHE_BAD_LENGTH, TF_CACHE_BAD_ROWS, TF_CACHE_TIMEOUT = 1, 2, 4, 8
 TF_FLAG_QK_NORM, TF_FLAG_QK_NORM_FAST, TF_FLAG_SLOW_CB_SUM, TF_FLAG_PAGED_KV = 1, 2, 4, 8
 
 
@@ -42,6 +44,16 @@ class TfInfo(ctypes.Structure):
                 ("num_sms", ctypes.c_int32), ("graph_nodes", ctypes.c_int32),
                 ("weight_bytes", ctypes.c_int64), ("frame_weight_bytes", ctypes.c_int64),
                 ("device_bytes", ctypes.c_int64)]
+
+
+class TfKvCache(ctypes.Structure):
+    """One layer's page pools and the batch a cache operator works on (tf_kv_cache)."""
+    _fields_ = [("format", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("K", ctypes.c_void_p), ("V", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int32),
+                ("n_seq", ctypes.c_int32), ("lengths", ctypes.c_void_p), ("row_start", ctypes.c_void_p),
+                ("n_rows", ctypes.c_int32), ("max_rows", ctypes.c_int32), ("max_length", ctypes.c_int32),
+                ("err", ctypes.c_void_p)]
 
 
 EXPORTS = {
@@ -100,6 +112,18 @@ EXPORTS = {
     "tf_op_gemv": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64,
                                   ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
                                   ctypes.POINTER(ctypes.c_float), ctypes.c_void_p]),
+    "tf_op_cache_page_bytes": (ctypes.c_int64, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
+    "tf_op_attention_cache": (ctypes.c_int, [ctypes.POINTER(TfKvCache), ctypes.c_void_p, ctypes.c_int64,
+                                             ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
+                                             ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                             ctypes.c_float, ctypes.c_void_p]),
+    "tf_op_cache_append": (ctypes.c_int, [ctypes.POINTER(TfKvCache), ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p]),
+    "tf_op_cache_read": (ctypes.c_int, [ctypes.POINTER(TfKvCache), ctypes.c_void_p, ctypes.c_void_p,
+                                        ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p]),
+    "tf_op_cache_copy": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                        ctypes.c_void_p]),
 }
 
 _LIB = None
@@ -324,3 +348,45 @@ def op_gemv(W_dev, dtype, scale_dev, rows, cols, x_dev, y_dev, repeat=1, stream=
     _check(lib().tf_op_gemv(W_dev, dtype, scale_dev, rows, cols, x_dev, y_dev, repeat,
                             ctypes.byref(ms), stream))
     return ms.value
+
+
+_KV_FORMATS = {"bf16": TF_KV_BF16, "nvfp4": TF_KV_NVFP4}
+_ROW_TYPES = {"bf16": TF_DTYPE_BF16, "f32": TF_DTYPE_F32}
+
+
+def kv_cache(fmt, n_kv_heads, head_dim, K_dev, V_dev, n_pages, table_dev, table_stride, n_seq, lengths_dev,
+             row_start_dev, n_rows, max_rows, max_length=0, err_dev=None) -> TfKvCache:
+    """The cache operators' description of one layer's pools ("bf16" or "nvfp4" pages) and a batch: sequence b
+    has the rows row_start[b] .. row_start[b + 1] - 1 at its last positions (row_start None: the row b).  The
+    caller keeps every array alive; a description may be used for any number of calls."""
+    return TfKvCache(_KV_FORMATS[fmt], n_kv_heads, head_dim, n_pages, K_dev, V_dev, table_dev, table_stride,
+                     n_seq, lengths_dev, row_start_dev, n_rows, max_rows, max_length, err_dev)
+
+
+def cache_page_bytes(fmt, n_kv_heads, head_dim) -> int:
+    return lib().tf_op_cache_page_bytes(_KV_FORMATS[fmt], n_kv_heads, head_dim)
+
+
+def op_attention_cache(cache, q_dev, out_dev, dtype, n_heads, window=0, sinks=0, scale=0.0, q_stride=0,
+                       out_stride=0, stream=0):
+    _check(lib().tf_op_attention_cache(cache, q_dev, q_stride, out_dev, out_stride, _ROW_TYPES[dtype],
+                                       n_heads, window, sinks, scale, stream))
+
+
+def op_cache_append(cache, k_dev, v_dev, dtype, stream=0, stride=0):
+    _check(lib().tf_op_cache_append(cache, k_dev, v_dev, stride, _ROW_TYPES[dtype], stream))
+
+
+def op_cache_read(cache, k_dev, v_dev, dtype, stream=0, stride=0):
+    _check(lib().tf_op_cache_read(cache, k_dev, v_dev, stride, _ROW_TYPES[dtype], stream))
+
+
+def op_cache_copy(pools, page_bytes, n_pages, src, dst, stream=0):
+    """Copies pages src[i] -> dst[i] (host ids) in every pool (device pointers)."""
+    bases = (ctypes.c_void_p * len(pools))(*pools)
+    src = np.ascontiguousarray(src, dtype=np.int32)
+    dst = np.ascontiguousarray(dst, dtype=np.int32)
+    if src.shape != dst.shape or src.ndim != 1:
+        raise ValueError("src and dst are lists of the same length")
+    _check(lib().tf_op_cache_copy(bases, len(pools), page_bytes, n_pages, src.ctypes.data, dst.ctypes.data,
+                                  src.size, stream))

@@ -344,4 +344,45 @@ cudaError_t launch_rmsnorm_rows(const float* x, const uint16_t* w, float* a, int
 cudaError_t launch_rmsnorm_split(const float* x, const uint16_t* w, uint16_t* hi, uint16_t* lo,
                                  int M, int H, float eps, cudaStream_t s);
 
+// ----------------------------------------------------------------- cache operators
+// A layer's page pools and the rows of a batch (tf_kv_cache, validated).
+struct CacheBatch {
+  int32_t fmt;             // 0 bf16, 1 4-bit
+  int32_t Hkv, D, n_pages;
+  const uint8_t* K;
+  const uint8_t* V;
+  const int32_t* tbl;      // [n_seq][npp]
+  int32_t npp, n_seq;
+  const int32_t* len;      // [n_seq]
+  const int32_t* row_start;  // [n_seq + 1] or null: sequence b has row b
+  int32_t n_rows, max_rows, max_len;
+  uint32_t* err;           // or null
+};
+struct CacheAttnParams {
+  CacheBatch c;
+  const void* q;
+  void* out;
+  int64_t q_stride, out_stride;  // elements
+  int32_t f32;             // rows are float32 (else bf16)
+  int32_t Hq, window, sinks;
+  float scale_log2;        // scale * log2(e)
+};
+struct CacheRowsParams {
+  CacheBatch c;
+  void* k;                 // rows read by append, written by read
+  void* v;
+  int64_t stride;          // elements
+  int32_t f32;
+};
+// Bytes of one KV head's page.
+inline int64_t cache_head_bytes(int fmt, int D) {
+  return fmt == 0 ? (int64_t)kKvPage * D * 2 : (int64_t)kKvPage * (D / 2 + D / 16 + 4);
+}
+cudaError_t launch_cache_attention(const CacheAttnParams& p, cudaStream_t s);
+cudaError_t launch_cache_append(const CacheRowsParams& p, cudaStream_t s);
+cudaError_t launch_cache_read(const CacheRowsParams& p, cudaStream_t s);
+// n copies of 16-byte words: page src[i] -> page dst[i] of every pool.
+cudaError_t launch_cache_copy(void* const* pools, int n_pools, int64_t page_bytes, const int32_t* src,
+                              const int32_t* dst, int n, cudaStream_t s);
+
 }  // namespace tf

@@ -1,0 +1,404 @@
+// Cache operators (sm_103a): rows appended to and read from a paged KV cache
+// in bfloat16 or 4 bits, page copies, and attention over the cache with a
+// sliding window and sinks.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "cache.cuh"
+#include "common.cuh"
+#include "device_once.h"
+#include "kernels.h"
+
+namespace tf {
+
+namespace {
+
+// ---------------------------------------------------------------- rows in and out
+// Half a warp takes one row of one head (D / 16 elements a lane), the two
+// halves of a warp the even and the odd position of a pair: a byte of V's
+// codes holds both positions of a pair, so one warp writes it whole.
+constexpr int kRowThreads = 128;
+
+template <int E>
+__device__ __forceinline__ void load_row(const void* base, size_t off, int f32, float (&x)[E]) {
+  if (f32) {
+    const float* p = static_cast<const float*>(base) + off;
+    if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+#pragma unroll
+      for (int i = 0; i < E; i += 4) *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(p + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) x[i] = p[i];
+    }
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + off;
+    if ((reinterpret_cast<uintptr_t>(p) & (E * 2 - 1)) == 0) {
+      uint32_t w[E / 2];
+      if constexpr (E == 8)
+        *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
+      else
+        *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        x[2 * i] = bf16_lo(w[i]);
+        x[2 * i + 1] = bf16_hi(w[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) x[i] = bf16_to_f32(p[i]);
+    }
+  }
+}
+
+template <int E>
+__device__ __forceinline__ void store_row(void* base, size_t off, int f32, const float (&x)[E]) {
+  if (f32) {
+    float* p = static_cast<float*>(base) + off;
+    if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+#pragma unroll
+      for (int i = 0; i < E; i += 4)
+        *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) p[i] = x[i];
+    }
+  } else {
+    uint16_t* p = static_cast<uint16_t*>(base) + off;
+#pragma unroll
+    for (int i = 0; i < E; ++i) p[i] = f32_to_bf16(x[i]);
+  }
+}
+
+// Largest of a half warp's values; a NaN anywhere gives a NaN.
+__device__ __forceinline__ float half_max_nan(float v, int from, int to) {
+  for (int o = from; o < to; o <<= 1) {
+    const float w = __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    v = (v != v || w != w) ? __int_as_float(0x7FFFFFFF) : fmaxf(v, w);
+  }
+  return v;
+}
+
+// e2m1 code of r in [-6, 6]: round to nearest, ties to the even code.
+__device__ __forceinline__ uint32_t e2m1_code(float r) {
+  const float a = fabsf(r);
+  const uint32_t m = (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) + (a >= 3.5f) + (a > 5.0f);
+  return m | (r < 0.0f ? 8u : 0u);
+}
+
+__device__ __forceinline__ float e2m1_value(uint32_t c) {
+  const uint32_t m = c & 7u;
+  const float a = m < 2 ? 0.5f * m : __uint_as_float((126u + (m >> 1)) << 23 | (m & 1u) << 22);
+  return (c & 8u) ? -a : a;
+}
+
+// x: a lane's E elements of a row.  Quantises them: codes (one per element),
+// the block's scale byte, the row's scale.
+template <int E>
+__device__ __forceinline__ void quantise_row(const float (&x)[E], uint32_t (&code)[E], uint32_t& sb, float& s) {
+  float am = 0.f;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    am = fmaxf(am, fabsf(x[i]));
+    bad |= !(fabsf(x[i]) < INFINITY);
+  }
+  if (bad) am = __int_as_float(0x7FFFFFFF);
+  const float blk = half_max_nan(am, 1, 16 / E);       // lanes of one block of 16
+  const float row = half_max_nan(blk, 16 / E, 16);     // the half warp
+  s = __fdiv_rn(row, 2688.0f);
+  const float s6 = __fmul_rn(s, 6.0f);
+  sb = 0;
+  float step = 0.f;
+  if (s6 > 0.f) {  // false for NaN
+    sb = __nv_cvt_float_to_fp8(fminf(__fdiv_rn(blk, s6), 448.0f), __NV_SATFINITE, __NV_E4M3);
+    step = __fmul_rn(e4m3_value(sb), s);
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    code[i] = step > 0.f ? e2m1_code(fminf(fmaxf(__fdiv_rn(x[i], step), -6.0f), 6.0f)) : 0u;
+}
+
+// Grid: (position pairs * KV heads, 2 (K, V), sequences); 4 warps a CTA.
+template <int D, int FMT>
+__global__ void __launch_bounds__(kRowThreads) k_cache_append(const CacheRowsParams p) {
+  constexpr int E = D / 16;
+  using L = Kv4<D>;
+  const CacheBatch& c = p.c;
+  const int b = blockIdx.z, isv = blockIdx.y;
+  const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
+  const SeqRows sq = cache_seq(c, b);
+  if (sq.n == 0) return;
+  const int p0 = max(sq.len - sq.n, 0);                 // first position written
+  const int item = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+  const int g = item % c.Hkv;
+  const int base = (p0 & ~1) + 2 * (item / c.Hkv);      // the pair's even position
+  if (base >= sq.len) return;
+  const int pos = base + half;
+  const bool mine = pos >= p0 && pos < sq.len;
+  const int page = cache_page(c, b, base / kKvPage);
+  if (page < 0) return;
+  const void* src = isv ? p.v : p.k;
+  float x[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) x[i] = 0.f;
+  if (mine)
+    load_row<E>(src, (size_t)(sq.r0 + pos - (sq.len - sq.n)) * p.stride + (size_t)g * D + l * E, p.f32, x);
+  const int r = pos % kKvPage;
+  uint8_t* pool = const_cast<uint8_t*>(isv ? c.V : c.K);
+  if constexpr (FMT == 0) {
+    uint16_t* dst = reinterpret_cast<uint16_t*>(pool) + (((size_t)page * c.Hkv + g) * kKvPage + r) * D + l * E;
+    if (mine) {
+      uint32_t w[E / 2];
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i)
+        w[i] = static_cast<uint32_t>(f32_to_bf16(x[2 * i])) | static_cast<uint32_t>(f32_to_bf16(x[2 * i + 1])) << 16;
+      if constexpr (E == 8)
+        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      else
+        *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    }
+  } else {
+    uint8_t* head = pool + ((size_t)page * c.Hkv + g) * L::kBytes;
+    uint32_t code[E], sb;
+    float s;
+    quantise_row<E>(x, code, sb, s);
+    if (mine && l == 0) reinterpret_cast<float*>(head + L::kRows)[r] = s;
+    const int blk = l * E / 16;
+    if (mine && (l * E) % 16 == 0)
+      head[L::kCodes + (isv ? blk * kKvPage + r : r * (D / 16) + blk)] = static_cast<uint8_t>(sb);
+    if (!isv) {
+      uint32_t w = 0;
+#pragma unroll
+      for (int i = 0; i < E; ++i) w |= code[i] << (4 * i);
+      if (mine) {
+        if constexpr (E == 8)
+          *reinterpret_cast<uint32_t*>(head + r * (D / 2) + l * 4) = w;
+        else
+          *reinterpret_cast<uint16_t*>(head + r * (D / 2) + l * 2) = static_cast<uint16_t>(w);
+      }
+    } else {
+      // the even position's lane writes the pair's bytes; a position that this
+      // call does not write keeps its nibble
+      uint32_t* dst = reinterpret_cast<uint32_t*>(head + L::v_byte(base % kKvPage, l * E));
+      const bool both = __shfl_xor_sync(0xFFFFFFFFu, mine ? 1 : 0, 16) && mine;
+#pragma unroll
+      for (int w = 0; w < E / 4; ++w) {
+        uint32_t v = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v |= code[4 * w + i] << (8 * i);
+        const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+        if (both) {
+          if (half == 0) dst[w] = v | (o << 4);
+        } else if (mine) {
+          dst[w] = half ? (dst[w] & 0x0F0F0F0Fu) | (v << 4) : (dst[w] & 0xF0F0F0F0u) | v;
+        }
+      }
+    }
+  }
+}
+
+// Value of a lane's E elements (from l * E) of position r of a 4-bit page.
+template <int D, int E>
+__device__ __forceinline__ void kv4_row(const uint8_t* head, int isv, int r, int l, float (&x)[E]) {
+  using L = Kv4<D>;
+  const int blk = l * E / 16;
+  const float sc = e4m3_value(head[L::kCodes + (isv ? blk * kKvPage + r : r * (D / 16) + blk)]);
+  const float s = reinterpret_cast<const float*>(head + L::kRows)[r];
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int d = l * E + i;
+    const uint32_t by = isv ? head[L::v_byte(r, d)] : head[r * (D / 2) + d / 2];
+    x[i] = e2m1_value(by >> (4 * ((isv ? r : d) & 1)) & 15u) * sc * s;
+  }
+}
+
+// Grid: (rows of a sequence * KV heads / 8, 2 (K, V), sequences).
+template <int D, int FMT>
+__global__ void __launch_bounds__(kRowThreads) k_cache_read(const CacheRowsParams p) {
+  constexpr int E = D / 16;
+  const CacheBatch& c = p.c;
+  const int b = blockIdx.z, isv = blockIdx.y;
+  const int l = threadIdx.x & 15;
+  const SeqRows sq = cache_seq(c, b);
+  const int item = blockIdx.x * (kRowThreads / 16) + (threadIdx.x >> 4);
+  const int i = item / c.Hkv, g = item % c.Hkv;
+  if (i >= sq.n) return;
+  const int pos = sq.len - sq.n + i;
+  float x[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = 0.f;
+  const int page = pos < 0 ? -1 : cache_page(c, b, pos / kKvPage);
+  if (page >= 0) {
+    const uint8_t* pool = isv ? c.V : c.K;
+    const int r = pos % kKvPage;
+    if constexpr (FMT == 0)
+      load_row<E>(pool, (((size_t)page * c.Hkv + g) * kKvPage + r) * D + l * E, 0, x);
+    else
+      kv4_row<D, E>(pool + ((size_t)page * c.Hkv + g) * Kv4<D>::kBytes, isv, r, l, x);
+  }
+  store_row<E>(isv ? p.v : p.k, (size_t)(sq.r0 + i) * p.stride + (size_t)g * D + l * E, p.f32, x);
+}
+
+// ---------------------------------------------------------------- page copies
+// The lists travel as kernel parameters, so a call needs no device staging.
+constexpr int kCopyPools = 128, kCopyMoves = 384;
+struct CopyParams {
+  uint4* pool[kCopyPools];
+  int2 move[kCopyMoves];
+  int32_t n_moves;
+  int32_t words;    // 16-byte words of a page
+  int32_t chunks;   // CTAs a page
+};
+constexpr int kCopyThreads = 256, kCopyUnroll = 4;
+
+__global__ void __launch_bounds__(kCopyThreads) k_cache_copy(const __grid_constant__ CopyParams p) {
+  const int m = blockIdx.x / p.chunks, ch = blockIdx.x % p.chunks;
+  uint4* pool = p.pool[blockIdx.y];
+  const uint4* src = pool + (size_t)p.move[m].x * p.words;
+  uint4* dst = pool + (size_t)p.move[m].y * p.words;
+  const int w0 = ch * kCopyThreads * kCopyUnroll + threadIdx.x;
+  uint4 v[kCopyUnroll];
+#pragma unroll
+  for (int u = 0; u < kCopyUnroll; ++u)
+    if (w0 + u * kCopyThreads < p.words) v[u] = src[w0 + u * kCopyThreads];
+#pragma unroll
+  for (int u = 0; u < kCopyUnroll; ++u)
+    if (w0 + u * kCopyThreads < p.words) dst[w0 + u * kCopyThreads] = v[u];
+}
+
+// ---------------------------------------------------------------- attention
+// One CTA per (query head, row): four warps take every fourth visible key,
+// lanes across the head dimension, an online softmax in registers; the warps
+// merge in shared memory.
+template <int D, int FMT>
+__global__ void __launch_bounds__(128) k_cache_attn_rows(const CacheAttnParams p) {
+  constexpr int E = D / 32;
+  const CacheBatch& c = p.c;
+  const int h = blockIdx.x, b = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = h / (p.Hq / c.Hkv);
+  __shared__ float sm_m[4], sm_l[4], sm_acc[4][D];
+  const SeqRows sq = cache_seq(c, b);
+  for (int i = blockIdx.y; i < sq.n; i += gridDim.y) {
+    const int pos = sq.len - sq.n + i;
+    const size_t qo = (size_t)(sq.r0 + i) * p.q_stride + (size_t)h * D + lane * E;
+    float q[E], acc[E], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      q[e] = p.f32 ? static_cast<const float*>(p.q)[qo + e] : bf16_to_f32(static_cast<const uint16_t*>(p.q)[qo + e]);
+      acc[e] = 0.f;
+    }
+    const int low = p.window > 0 ? max(0, pos - p.window + 1) : 0;  // window: keys low .. pos
+    const int sinks = p.window > 0 ? min(p.sinks, low) : 0;         // and keys 0 .. sinks - 1
+    const int n = sinks + max(0, pos + 1 - low);
+    for (int t = warp; t < n; t += 4) {
+      const int j = t < sinks ? t : low + t - sinks;
+      const int page = cache_page(c, b, j / kKvPage);
+      if (page < 0) continue;
+      const int r = j % kKvPage;
+      float k[E], v[E];
+      if constexpr (FMT == 0) {
+        const size_t o = (((size_t)page * c.Hkv + g) * kKvPage + r) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          k[e] = bf16_to_f32(reinterpret_cast<const uint16_t*>(c.K)[o + e]);
+          v[e] = bf16_to_f32(reinterpret_cast<const uint16_t*>(c.V)[o + e]);
+        }
+      } else {
+        const size_t o = ((size_t)page * c.Hkv + g) * Kv4<D>::kBytes;
+        kv4_row<D, E>(c.K + o, 0, r, lane, k);
+        kv4_row<D, E>(c.V + o, 1, r, lane, v);
+      }
+      float z = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) z = fmaf(q[e], k[e], z);
+      z = warp_sum(z) * p.scale_log2;
+      const float mn = fmaxf(m, z);
+      const float f = m == -INFINITY ? 0.f : exp2f(m - mn), w = exp2f(z - mn);
+      l = l * f + w;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], f, w * v[e]);
+      m = mn;
+    }
+    if (lane == 0) {
+      sm_m[warp] = m;
+      sm_l[warp] = l;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) sm_acc[warp][lane * E + e] = acc[e];
+    __syncthreads();
+    const float M = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
+    for (int d = threadIdx.x; d < D; d += 128) {
+      float A = 0.f, L = 0.f;
+      for (int w = 0; w < 4; ++w) {
+        const float f = sm_l[w] == 0.f ? 0.f : exp2f(sm_m[w] - M);
+        A += f * sm_acc[w][d];
+        L += f * sm_l[w];
+      }
+      const float o = L == 0.f ? 0.f : A / L;
+      const size_t oo = (size_t)(sq.r0 + i) * p.out_stride + (size_t)h * D + d;
+      if (p.f32)
+        static_cast<float*>(p.out)[oo] = o;
+      else
+        static_cast<uint16_t*>(p.out)[oo] = f32_to_bf16(o);
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace
+
+#define TF_CACHE_DISPATCH(KERNEL, GRID, BLOCK, S, P)                   \
+  do {                                                                 \
+    if ((P).c.D == 128)                                                \
+      (P).c.fmt ? KERNEL<128, 1><<<GRID, BLOCK, 0, S>>>(P)             \
+                : KERNEL<128, 0><<<GRID, BLOCK, 0, S>>>(P);            \
+    else                                                               \
+      (P).c.fmt ? KERNEL<64, 1><<<GRID, BLOCK, 0, S>>>(P)              \
+                : KERNEL<64, 0><<<GRID, BLOCK, 0, S>>>(P);             \
+  } while (0)
+
+cudaError_t launch_cache_append(const CacheRowsParams& p, cudaStream_t s) {
+  const int64_t items = ((int64_t)p.c.max_rows / 2 + 1) * p.c.Hkv;  // pairs that max_rows rows can touch
+  const int per = kRowThreads / 32;
+  const dim3 grid(static_cast<unsigned>((items + per - 1) / per), 2, p.c.n_seq);
+  TF_CACHE_DISPATCH(k_cache_append, grid, kRowThreads, s, p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_read(const CacheRowsParams& p, cudaStream_t s) {
+  const int64_t items = (int64_t)p.c.max_rows * p.c.Hkv;
+  const int per = kRowThreads / 16;
+  const dim3 grid(static_cast<unsigned>((items + per - 1) / per), 2, p.c.n_seq);
+  TF_CACHE_DISPATCH(k_cache_read, grid, kRowThreads, s, p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_copy(void* const* pools, int n_pools, int64_t page_bytes, const int32_t* src,
+                              const int32_t* dst, int n, cudaStream_t s) {
+  CopyParams p;
+  p.words = static_cast<int32_t>(page_bytes / 16);
+  p.chunks = (p.words + kCopyThreads * kCopyUnroll - 1) / (kCopyThreads * kCopyUnroll);
+  for (int q0 = 0; q0 < n_pools; q0 += kCopyPools) {
+    const int nq = std::min(kCopyPools, n_pools - q0);
+    for (int i = 0; i < nq; ++i) p.pool[i] = static_cast<uint4*>(pools[q0 + i]);
+    for (int m0 = 0; m0 < n; m0 += kCopyMoves) {
+      p.n_moves = std::min(kCopyMoves, n - m0);
+      for (int i = 0; i < p.n_moves; ++i) p.move[i] = make_int2(src[m0 + i], dst[m0 + i]);
+      k_cache_copy<<<dim3(p.n_moves * p.chunks, nq), kCopyThreads, 0, s>>>(p);
+      const cudaError_t e = cudaGetLastError();
+      if (e) return e;
+    }
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_cache_attention(const CacheAttnParams& p, cudaStream_t s) {
+  const dim3 grid(p.Hq, std::min(p.c.max_rows, 65535), p.c.n_seq);
+  TF_CACHE_DISPATCH(k_cache_attn_rows, grid, 128, s, p);
+  return cudaGetLastError();
+}
+
+}  // namespace tf

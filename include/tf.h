@@ -19,7 +19,8 @@
  *     soon as the call returns.  The library owns all device memory it
  *     allocates (tf_create) and frees it in tf_destroy.
  *   - Calls are synchronous with respect to the host: outputs are valid on
- *     return.  Work runs on the context's stream (tf_set_stream).
+ *     return (the cache operators at the end of this file only enqueue).
+ *     Work runs on the context's stream (tf_set_stream).
  *   - A context is used by one host thread at a time.
  *   - Errors: every call returns a tf_status; tf_last_error() gives a one-line
  *     message.  After TF_E_CUDA or TF_E_TIMEOUT the context is poisoned and
@@ -60,8 +61,9 @@ typedef enum {
 enum { TF_WEIGHT_BF16 = 0, TF_WEIGHT_FP8 = 1, TF_WEIGHT_NVFP4 = 2 };
 /* Element types of tensors handed to tf_load_weights (tf_tensor.dtype), and
  * of the weight given to tf_op_gemv (TF_DTYPE_NVFP4: rows as
- * tf_op_quantize_nvfp4 writes them). */
-enum { TF_DTYPE_BF16 = 0, TF_DTYPE_FP8_E4M3 = 1, TF_DTYPE_NVFP4 = 2 };
+ * tf_op_quantize_nvfp4 writes them).  TF_DTYPE_F32 and TF_DTYPE_BF16 are the
+ * row types of the cache operators. */
+enum { TF_DTYPE_BF16 = 0, TF_DTYPE_FP8_E4M3 = 1, TF_DTYPE_NVFP4 = 2, TF_DTYPE_F32 = 3 };
 
 /* Model shape.  All sizes are element counts.
  * head_dim must be 64 or 128; n_heads a multiple of n_kv_heads with
@@ -435,6 +437,120 @@ tf_status tf_op_gemm_skinny_nvfp4(const float* A, const uint8_t* W, const float*
 tf_status tf_op_gemv(const void* W, int32_t dtype, const float* row_scale,
                      int64_t rows, int64_t cols, const float* x, float* y,
                      int32_t repeat, float* ms, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Cache operators for serving: attention over a paged KV cache held in
+ * bfloat16 or in 4 bits, with a sliding window and sinks; rows appended to and
+ * read from such a cache; pages copied.  (The fish-s2-pro-mlx-local-deploy
+ * README's architecture paragraph and the drbaph s2-pro-fp8 card's
+ * "Architecture" name continuous batching with a paged KV cache for serving;
+ * window, sinks and the 4-bit cache have no counterpart in the pages.)
+ *
+ * Unlike the calls above these do not synchronise: they enqueue on `stream`
+ * (cudaStream_t, NULL = legacy default stream) of the current device, allocate
+ * nothing, keep nothing from one call to the next and use no shared
+ * workspace, so calls on several streams do not disturb one another and every
+ * call can be captured into a CUDA graph (the device arrays that a call names
+ * are read when it runs).  Arguments on the host are checked before anything
+ * is enqueued; what only the device can see (block table, lengths, row_start)
+ * is checked there and reported in tf_kv_cache.err.
+ *
+ * A pool holds pages of 32 positions: [page][n_kv_heads][bytes of one head].
+ * TF_KV_BF16: 32 rows of head_dim bfloat16 (the layout of TF_FLAG_PAGED_KV).
+ * TF_KV_NVFP4: 32*D/2 bytes of e2m1 codes, then 32*D/16 e4m3 block scales,
+ *   then 32 float32 row scales (D = head_dim).  A row (one position's K or V
+ *   of one head) is quantised as tf_op_quantize_nvfp4 does a weight row,
+ *   except that the scale of a row of zeros is 0: s = amax / 2688, b =
+ *   e4m3(min(amax of 16 / (6 s), 448)), code = e2m1(clamp(x / (b s), -6, 6)),
+ *   each step one float32 operation; the value is e2m1 * b * s.  A row with an
+ *   infinity or a NaN gets the row scale NaN (and zero codes).
+ *   K pool: codes [32][D/2], the even element in the low nibble; block scales
+ *     [32][D/16].
+ *   V pool, with position 8t + 2j + i of the page (t < 4, j < 4, i < 2): codes
+ *     [j][D/16][t][16] bytes, one element per byte, i = 0 in the low nibble
+ *     and i = 1 in the high one; block scales [D/16][32].  (Two positions of
+ *     one element share a byte, in the order in which the attention's matrix
+ *     products take them.)
+ * ------------------------------------------------------------------------- */
+enum { TF_KV_BF16 = 0, TF_KV_NVFP4 = 1 };
+/* Bits of tf_kv_cache.err. */
+enum {
+  TF_CACHE_BAD_PAGE = 1,    /* a block-table entry outside [0, n_pages) that a row needs: attention
+                               takes its positions as hidden, append skips them, read gives zeros */
+  TF_CACHE_BAD_LENGTH = 2,  /* a length below 0 or above 32*table_stride: that sequence is skipped   */
+  TF_CACHE_BAD_ROWS = 4,    /* row_start falls, leaves [0, n_rows] or gives a sequence more than
+                               max_rows rows: that sequence is skipped                               */
+  TF_CACHE_TIMEOUT = 8      /* a bounded wait inside the kernel expired: outputs are not valid       */
+};
+
+/* One layer's pools and the batch that a call works on.  All pointers are
+ * device pointers. */
+typedef struct {
+  int32_t format;             /* TF_KV_*                                                       */
+  int32_t n_kv_heads;         /* KV heads                                                      */
+  int32_t head_dim;           /* 64 or 128                                                     */
+  int32_t n_pages;            /* pages in each pool; n_pages * n_kv_heads * 32 < 2^31          */
+  void* K;                    /* the pools, 128-byte aligned                                   */
+  void* V;
+  const int32_t* block_table; /* [n_seq][table_stride]: page of positions 32 i .. 32 i + 31    */
+  int32_t table_stride;
+  int32_t n_seq;              /* sequences of this call, 1..65535                              */
+  const int32_t* lengths;     /* [n_seq]: positions cached, the call's own rows included       */
+  const int32_t* row_start;   /* [n_seq + 1]: sequence b's rows are row_start[b] ..
+                                 row_start[b + 1] - 1, its last ones: row i sits at position
+                                 lengths[b] - (row_start[b + 1] - i).  NULL: sequence b has
+                                 the one row b                                                */
+  int32_t n_rows;             /* rows in the row buffers (rows past the last sequence's are
+                                 neither read nor written)                                    */
+  int32_t max_rows;           /* no sequence has more rows than this                           */
+  int32_t max_length;         /* lengths are about this at most (sizes the launch; any value is
+                                 correct); 0: 32*table_stride                                  */
+  uint32_t* err;              /* NULL, or a word into which TF_CACHE_* bits are OR-ed          */
+} tf_kv_cache;
+
+/* Bytes of one page of a K or a V pool (all KV heads); 0 for bad arguments. */
+int64_t tf_op_cache_page_bytes(int32_t format, int32_t n_kv_heads, int32_t head_dim);
+
+/* Grouped-query attention of every sequence's last rows over its cached
+ * positions: the row at position p sees position j if j <= p and (window = 0,
+ * or j > p - window, or j < sinks); out = sum softmax(scale q.K) V over what it
+ * sees, and zeros for a row that sees nothing (a negative position).  Positions
+ * that a row does not see do not touch it, whatever their pages hold.
+ * q, out: [n_rows] rows of n_heads*D elements, q_stride and out_stride elements
+ * apart (0: n_heads*D), of type `dtype` (TF_DTYPE_F32 or TF_DTYPE_BF16); query
+ * head h reads KV head h / (n_heads / n_kv_heads), a ratio of 1 to 8.  out must
+ * not overlap q or the pools.  scale > 0 (0: 1/sqrt(D)).
+ * Scores, softmax statistics and sums are float32; with TF_DTYPE_F32 queries
+ * and probabilities enter the matrix products with 22 or more significant
+ * bits, with TF_DTYPE_BF16 the probabilities enter as bfloat16 or float16.
+ * Errors: TF_E_INVAL, TF_E_CUDA. */
+tf_status tf_op_attention_cache(const tf_kv_cache* cache, const void* q, int64_t q_stride, void* out,
+                                int64_t out_stride, int32_t dtype, int32_t n_heads, int32_t window,
+                                int32_t sinks, float scale, void* stream);
+
+/* Writes the sequences' rows k, v ([n_rows] rows of n_kv_heads*D elements,
+ * `stride` elements apart, 0: n_kv_heads*D) to their positions in the pools,
+ * rounded to bfloat16 or quantised; rows at negative positions are skipped.
+ * Two sequences of a call must not name the same page for positions that both
+ * write.  Errors: TF_E_INVAL, TF_E_CUDA. */
+tf_status tf_op_cache_append(const tf_kv_cache* cache, const void* k, const void* v, int64_t stride,
+                             int32_t dtype, void* stream);
+
+/* The inverse: the values that the pools hold at the rows' positions, written
+ * to k, v (same layout; zeros for rows at negative positions).
+ * Errors: TF_E_INVAL, TF_E_CUDA. */
+tf_status tf_op_cache_read(const tf_kv_cache* cache, void* k, void* v, int64_t stride, int32_t dtype,
+                           void* stream);
+
+/* Copies page src[i] onto page dst[i], i < n, in each of n_pools pools (device
+ * pointers pools[], 16-byte aligned, of n_pages pages of page_bytes bytes each,
+ * a multiple of 16): the pages a forked sequence needs of its own, or live
+ * pages moved down before a pool shrinks.  src, dst and pools are HOST arrays,
+ * taken by value.  A page may be the source of several copies, but no page may
+ * be a destination twice, or a destination and a source (copies run in no
+ * order).  Errors: TF_E_INVAL, TF_E_CUDA. */
+tf_status tf_op_cache_copy(void* const* pools, int32_t n_pools, int64_t page_bytes, int32_t n_pages,
+                           const int32_t* src, const int32_t* dst, int32_t n, void* stream);
 
 #ifdef __cplusplus
 }
