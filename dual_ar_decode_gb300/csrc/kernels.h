@@ -378,7 +378,8 @@ struct CacheRowsParams {
 inline int64_t cache_head_bytes(int fmt, int D) {
   return fmt == 0 ? (int64_t)kKvPage * D * 2 : (int64_t)kKvPage * (D / 2 + D / 16 + 4);
 }
-cudaError_t launch_cache_attention(const CacheAttnParams& p, cudaStream_t s);
+// Few rows per sequence (any number is right).
+cudaError_t launch_cache_decode(const CacheAttnParams& p, cudaStream_t s);
 cudaError_t launch_cache_append(const CacheRowsParams& p, cudaStream_t s);
 cudaError_t launch_cache_read(const CacheRowsParams& p, cudaStream_t s);
 // n copies of 16-byte words: page src[i] -> page dst[i] of every pool.

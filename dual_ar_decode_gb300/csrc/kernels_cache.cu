@@ -1,6 +1,5 @@
 // Cache operators (sm_103a): rows appended to and read from a paged KV cache
-// in bfloat16 or 4 bits, page copies, and attention over the cache with a
-// sliding window and sinks.
+// in bfloat16 or 4 bits, and page copies.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -268,86 +267,6 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache_copy(const __grid_consta
     if (w0 + u * kCopyThreads < p.words) dst[w0 + u * kCopyThreads] = v[u];
 }
 
-// ---------------------------------------------------------------- attention
-// One CTA per (query head, row): four warps take every fourth visible key,
-// lanes across the head dimension, an online softmax in registers; the warps
-// merge in shared memory.
-template <int D, int FMT>
-__global__ void __launch_bounds__(128) k_cache_attn_rows(const CacheAttnParams p) {
-  constexpr int E = D / 32;
-  const CacheBatch& c = p.c;
-  const int h = blockIdx.x, b = blockIdx.z;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = h / (p.Hq / c.Hkv);
-  __shared__ float sm_m[4], sm_l[4], sm_acc[4][D];
-  const SeqRows sq = cache_seq(c, b);
-  for (int i = blockIdx.y; i < sq.n; i += gridDim.y) {
-    const int pos = sq.len - sq.n + i;
-    const size_t qo = (size_t)(sq.r0 + i) * p.q_stride + (size_t)h * D + lane * E;
-    float q[E], acc[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      q[e] = p.f32 ? static_cast<const float*>(p.q)[qo + e] : bf16_to_f32(static_cast<const uint16_t*>(p.q)[qo + e]);
-      acc[e] = 0.f;
-    }
-    const int low = p.window > 0 ? max(0, pos - p.window + 1) : 0;  // window: keys low .. pos
-    const int sinks = p.window > 0 ? min(p.sinks, low) : 0;         // and keys 0 .. sinks - 1
-    const int n = sinks + max(0, pos + 1 - low);
-    for (int t = warp; t < n; t += 4) {
-      const int j = t < sinks ? t : low + t - sinks;
-      const int page = cache_page(c, b, j / kKvPage);
-      if (page < 0) continue;
-      const int r = j % kKvPage;
-      float k[E], v[E];
-      if constexpr (FMT == 0) {
-        const size_t o = (((size_t)page * c.Hkv + g) * kKvPage + r) * D + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          k[e] = bf16_to_f32(reinterpret_cast<const uint16_t*>(c.K)[o + e]);
-          v[e] = bf16_to_f32(reinterpret_cast<const uint16_t*>(c.V)[o + e]);
-        }
-      } else {
-        const size_t o = ((size_t)page * c.Hkv + g) * Kv4<D>::kBytes;
-        kv4_row<D, E>(c.K + o, 0, r, lane, k);
-        kv4_row<D, E>(c.V + o, 1, r, lane, v);
-      }
-      float z = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) z = fmaf(q[e], k[e], z);
-      z = warp_sum(z) * p.scale_log2;
-      const float mn = fmaxf(m, z);
-      const float f = m == -INFINITY ? 0.f : exp2f(m - mn), w = exp2f(z - mn);
-      l = l * f + w;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], f, w * v[e]);
-      m = mn;
-    }
-    if (lane == 0) {
-      sm_m[warp] = m;
-      sm_l[warp] = l;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) sm_acc[warp][lane * E + e] = acc[e];
-    __syncthreads();
-    const float M = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
-    for (int d = threadIdx.x; d < D; d += 128) {
-      float A = 0.f, L = 0.f;
-      for (int w = 0; w < 4; ++w) {
-        const float f = sm_l[w] == 0.f ? 0.f : exp2f(sm_m[w] - M);
-        A += f * sm_acc[w][d];
-        L += f * sm_l[w];
-      }
-      const float o = L == 0.f ? 0.f : A / L;
-      const size_t oo = (size_t)(sq.r0 + i) * p.out_stride + (size_t)h * D + d;
-      if (p.f32)
-        static_cast<float*>(p.out)[oo] = o;
-      else
-        static_cast<uint16_t*>(p.out)[oo] = f32_to_bf16(o);
-    }
-    __syncthreads();
-  }
-}
-
 }  // namespace
 
 #define TF_CACHE_DISPATCH(KERNEL, GRID, BLOCK, S, P)                   \
@@ -393,12 +312,6 @@ cudaError_t launch_cache_copy(void* const* pools, int n_pools, int64_t page_byte
     }
   }
   return cudaSuccess;
-}
-
-cudaError_t launch_cache_attention(const CacheAttnParams& p, cudaStream_t s) {
-  const dim3 grid(p.Hq, std::min(p.c.max_rows, 65535), p.c.n_seq);
-  TF_CACHE_DISPATCH(k_cache_attn_rows, grid, 128, s, p);
-  return cudaGetLastError();
 }
 
 }  // namespace tf

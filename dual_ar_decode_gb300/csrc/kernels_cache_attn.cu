@@ -1,0 +1,832 @@
+// Attention of few rows per sequence over a paged KV cache (sm_103a): the
+// decode form of tf_op_attention_cache, for bf16 and 4-bit pages.
+//
+// out = sum_j p_j v_j with p = softmax_j(scale q.k_j) over the positions a row
+// sees (window and sinks).  One row reads every visible K and V row of its KV
+// head once and does 4 D flops per (head, position): memory is the bound, so
+// the work is laid out to keep HBM busy and to spend few instructions per
+// cached element.
+//
+//   * A group is (sequence, KV head, tile of 8 NT columns); a column is one
+//     (row, query head) pair, so all heads of a KV head (and up to 4 rows more)
+//     share each K and V read.  A cluster of up to 16 CTAs takes one group and
+//     splits its list of pages; the CTAs' partial softmax results meet in
+//     distributed shared memory in rank order.  So there is no workspace, no
+//     second launch and no atomic, and calls on several streams cannot meet.
+//   * Every warp streams its own pages through its own ring of shared-memory
+//     stages (bulk copies of a head's contiguous 4-bit page, TMA boxes with the
+//     128-byte swizzle for bf16): no CTA barrier inside the loop.
+//   * Scores and outputs are computed as S^T = K q^T and O^T = V^T P^T with
+//     mma.sync m16n8k16: keys (or head dims) on the 16-row side, columns on the
+//     8-wide side.  With 8 columns a tcgen05 tile (M = 128 keys, N = 8) would
+//     need its operands in shared memory in its own layout, i.e. one more trip
+//     of the dequantised elements; here they go from the conversion's registers
+//     into the product.  The tensor pipe is at half load at most.
+//   * 4-bit elements: e2m1 x e4m3 has at most 6 significant bits and is exact in
+//     f16 (values 2^-10 .. 2688), so a page costs one conversion and one multiply
+//     per two elements, and row scales are applied to scores and probabilities
+//     in float32.  Queries are scaled by a power of two into f16's range and
+//     split in f16 hi + lo (22 bits); the probability times V's row scale is
+//     split the same way against a running reference (see below).  bf16 pages:
+//     three bf16 parts (24 bits) for float32 rows.
+//   * The maximum m (and, for 4-bit pages, the reference A of the outputs) is
+//     replaced only when a score exceeds it by more than 2^8, which one vote per
+//     page finds: in the steady state a page needs no shuffles.
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "cache.cuh"
+#include "common.cuh"
+#include "device_once.h"
+#include "kernels.h"
+#include "tensor_map.h"
+
+namespace tf {
+
+namespace {
+
+constexpr float kGrow = 8.0f;  // log2 of the growth at which a reference is replaced
+// 4-bit pages: the weights p * (V's row scale) are multiplied in f16 parts, relative to a reference 2^A
+// that puts the largest at 2^7 when it is set and lets it grow to 2^15.
+constexpr float kRefBits = 7.0f, kRefTop = 15.0f;
+constexpr float kTiny = 1.92592994e-34f;  // 2^-112: weights below it count as zero
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2f(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Bounded wait that only reports (the caller decides what to do).
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer_ns() - t0 > kWaitBudgetNs) return false;
+  return true;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+
+template <int FMT>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  if constexpr (FMT == 0)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// Four bytes of e2m1 pairs -> four f16x2 (low nibble in the low half).
+__device__ __forceinline__ void e2m1x8(uint32_t v, uint32_t (&h)[4]) {
+  asm("{.reg .b8 b0, b1, b2, b3; mov.b32 {b0, b1, b2, b3}, %4;"
+      " cvt.rn.f16x2.e2m1x2 %0, b0; cvt.rn.f16x2.e2m1x2 %1, b1;"
+      " cvt.rn.f16x2.e2m1x2 %2, b2; cvt.rn.f16x2.e2m1x2 %3, b3;}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(v));
+}
+__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t v) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(v)));
+  return h;
+}
+__device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// (x, y) -> NP parts of 16 bits each whose sum is the pair: part 0 is the
+// rounded value, the next the rounded remainder, ...; f16 (FMT 1) or bf16.
+template <int FMT, int NP>
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t (&part)[NP]) {
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    uint32_t h;
+    if constexpr (FMT == 0)
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(y), "f"(x));
+    else
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(y), "f"(x));
+    part[i] = h;
+    if (i + 1 < NP) {
+      if constexpr (FMT == 0) {
+        x -= bf16_lo(h);
+        y -= bf16_hi(h);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        x -= f.x;
+        y -= f.y;
+      }
+    }
+  }
+}
+
+// Shared memory and shape of one instantiation.
+template <int D, int FMT, int NT, int F32>
+struct DecCfg {
+  static constexpr int kWarps = 8;
+  static constexpr int kKeys = FMT ? 32 : 16;               // positions of a stage (a page, or half a page)
+  static constexpr int kHalf = FMT ? Kv4<D>::kBytes : 16 * D * 2;  // K (or V) bytes of a stage
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kStages = FMT ? 2 : (D == 64 ? 4 : NT == 4 ? 2 : 3);
+  static constexpr int kQp = FMT ? (F32 ? 2 : 1) : (F32 ? 3 : 1);  // parts of a query
+  static constexpr int kPp = FMT ? (F32 ? 2 : 1) : (F32 ? 3 : 2);  // parts of a probability
+  static constexpr int kSteps = D / 16;
+  static constexpr int kCols = 8 * NT;
+  static constexpr int kLd = D + 8;                         // row of a warp's partial outputs
+  static constexpr size_t kRing = (size_t)kWarps * kStages * kStage;
+  static constexpr size_t kParts = (size_t)kWarps * kCols * kLd * 4;  // overlays the ring at the end
+  static constexpr size_t kOffQ = ((kRing > kParts ? kRing : kParts) + 127) / 128 * 128;
+  static constexpr size_t kOffC = kOffQ + (size_t)NT * kQp * kSteps * 32 * 8;  // the CTA's partial [kCols][D]
+  static constexpr size_t kOffStat = kOffC + (size_t)kCols * D * 4;
+  // per warp and column: reference of the outputs, maximum, sum; per column: the CTA's maximum and sum; scale
+  static constexpr size_t kOffBar = kOffStat + (size_t)(3 * kWarps + 3) * kCols * 4;
+  static constexpr size_t kSmem = 1024 + kOffBar + kWarps * kStages * 8 + 16;
+};
+
+struct TileRows {
+  int r0, n, len;     // the sequence's rows and length
+  int c0, nc;         // the tile's first column and how many it has
+};
+
+template <int D, int FMT, int NT, int F32>
+__global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
+    k_cache_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                   const CacheAttnParams p, const int csize) {
+  using C = DecCfg<D, FMT, NT, F32>;
+  constexpr int KB = C::kKeys / 8;   // blocks of 8 keys in a stage
+  constexpr int MT = D / 16;         // 16-row tiles of the head dimension
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const CacheBatch& c = p.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = lane >> 2, lt = lane & 3;
+  const int rank = static_cast<int>(blockIdx.x) % csize, tile = static_cast<int>(blockIdx.x) / csize;
+  const int hkv = blockIdx.y, b = blockIdx.z;
+  const int G = p.Hq / c.Hkv;
+  const SeqRows sq = cache_seq(c, b);
+  const int c0 = tile * C::kCols;
+  const int ncol = min(C::kCols, sq.n * G - c0);
+  if (ncol <= 0) return;  // the whole cluster
+  const int first = sq.len - sq.n;                       // position of the sequence's row 0
+  const int posmin = first + c0 / G, posmax = first + (c0 + ncol - 1) / G;
+  const bool win = p.window > 0;
+  const int lowmin = win ? max(0, posmin - p.window + 1) : 0;
+  const int lowmax = win ? max(0, posmax - p.window + 1) : 0;
+  const int sinks = win ? p.sinks : 0;
+
+  // The list of stages: those of the sinks that the windows do not reach, then lowmin .. posmax.
+  const int ulow = lowmin / C::kKeys;
+  const int usink = min(ulow, (min(sinks, lowmin) + C::kKeys - 1) / C::kKeys);
+  const int units = posmax < 0 ? 0 : usink + posmax / C::kKeys - ulow + 1;
+
+  float* cpart = reinterpret_cast<float*>(smem + C::kOffC);
+  float* wref = reinterpret_cast<float*>(smem + C::kOffStat);   // [warp][col]
+  float* wmax = wref + C::kWarps * C::kCols;
+  float* wsum = wmax + C::kWarps * C::kCols;
+  float* cmax = wsum + C::kWarps * C::kCols;                    // [col]
+  float* csum = cmax + C::kCols;
+  float* qscale = csum + C::kCols;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar) + warp * C::kStages;
+  uint8_t* ring = smem + (size_t)warp * C::kStages * C::kStage;
+
+  if (lane == 0) {
+    for (int s = 0; s < C::kStages; ++s) mbar_init(&bars[s], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+
+  // ---- this warp's stages: gw, gw + nw, ...
+  const int gw = rank * C::kWarps + warp, nw = csize * C::kWarps;
+  const int mine = gw < units ? (units - gw + nw - 1) / nw : 0;
+  auto unit_at = [&](int i) {
+    const int u = gw + i * nw;
+    return u < usink ? u : ulow + u - usink;
+  };
+  // page ids of up to 32 stages ahead, one per lane
+  int ids = -1;
+  auto look_up = [&](int from) {
+    const int i = from + lane;
+    ids = i < mine ? cache_page(c, b, unit_at(i) / (kKvPage / C::kKeys)) : -1;
+  };
+  auto issue = [&](int i) {  // all lanes; stage i of this warp into ring slot i % kStages
+    if ((i & 31) == 0) look_up(i);
+    const int page = __shfl_sync(0xFFFFFFFFu, ids, i & 31);
+    if (lane == 0) {
+      const int s = i % C::kStages;
+      const uint32_t dst = smem_u32(ring + (size_t)s * C::kStage);
+      if (page < 0) {
+        mbar_arrive(&bars[s]);  // nothing to wait for; the stage is skipped
+      } else if constexpr (FMT == 1) {
+        const size_t off = ((size_t)page * c.Hkv + hkv) * C::kHalf;
+        mbar_arrive_expect_tx(&bars[s], C::kStage);
+        bulk_load(dst, c.K + off, C::kHalf, &bars[s]);
+        bulk_load(dst + C::kHalf, c.V + off, C::kHalf, &bars[s]);
+      } else {
+        const int y = (page * c.Hkv + hkv) * kKvPage + (unit_at(i) % (kKvPage / C::kKeys)) * C::kKeys;
+        mbar_arrive_expect_tx(&bars[s], C::kStage);
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) {
+          tma_box(dst + x * (16 * 128), &map_k, x * 64, y, &bars[s]);
+          tma_box(dst + C::kHalf + x * (16 * 128), &map_v, x * 64, y, &bars[s]);
+        }
+      }
+    }
+    return page;
+  };
+  uint32_t good = 0;  // bit s: slot s holds a page of the pool
+  for (int i = 0; i < min(mine, C::kStages); ++i) good |= (issue(i) >= 0 ? 1u : 0u) << (i % C::kStages);
+
+  // ---- queries: the parts of every column in the order the products read them.  A column's queries are
+  // scaled by a power of two so that the largest is in [2^14, 2^15) (FMT 1: f16 holds them).
+  for (int col = warp; col < C::kCols; col += C::kWarps) {
+    const int cc = c0 + col, row = cc / G, h = hkv * G + cc % G;
+    float x[D / 32];  // dims lane, lane + 32, ...
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) {
+      x[e] = 0.f;
+      if (col < ncol) {
+        const size_t o = (size_t)(sq.r0 + row) * p.q_stride + (size_t)h * D + lane + 32 * e;
+        x[e] = F32 ? static_cast<const float*>(p.q)[o] : bf16_to_f32(static_cast<const uint16_t*>(p.q)[o]);
+      }
+    }
+    float up = 1.f;
+    if constexpr (FMT == 1) {
+      float am = 0.f;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) am = fmaxf(am, fabsf(x[e]));
+      am = warp_max(am);
+      const int ex = static_cast<int>(__float_as_uint(am) >> 23) - 127;  // floor(log2 am); -127: zero or tiny
+      const int sh = min(126, max(-126, 14 - ex));
+      up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+      if (lane == 0) qscale[col] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+    } else if (lane == 0) {
+      qscale[col] = p.scale_log2;
+    }
+    uint16_t* qf = reinterpret_cast<uint16_t*>(smem + C::kOffQ);
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) {
+      const int d = lane + 32 * e;
+      // place of element d in the products: step s, lane quarter t, half (b0 / b1), low or high
+      int s, t, hf, lo;
+      if constexpr (FMT == 1) {
+        constexpr int per = D / 4;  // a lane's elements of a row are consecutive
+        t = d / per;
+        s = d % per / 4;
+        hf = d % 4 / 2;
+        lo = d % 2;
+      } else {
+        s = d / 16;
+        hf = d % 16 / 8;
+        t = d % 8 / 2;
+        lo = d % 2;
+      }
+      uint32_t part[C::kQp];
+      split_pair<FMT, C::kQp>(x[e] * up, 0.f, part);
+#pragma unroll
+      for (int q = 0; q < C::kQp; ++q)
+        qf[((((size_t)(col / 8) * C::kQp + q) * C::kSteps + s) * 32 + (col % 8) * 4 + t) * 4 + hf * 2 + lo] =
+            static_cast<uint16_t>(part[q]);
+    }
+  }
+  __syncthreads();
+  const uint2* qf = reinterpret_cast<const uint2*>(smem + C::kOffQ) + lane;
+
+  // ---- this lane's columns 2 lt, 2 lt + 1 of every n-tile
+  int pos[NT][2], low[NT][2];
+  float cs[NT][2], m[NT][2], mref[NT][2], l[NT][2];
+  float A[NT][2], F[NT][2], thr[NT][2];  // FMT 1: reference of the outputs
+  float o[NT][MT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int col = n * 8 + 2 * lt + e;
+      pos[n][e] = col < ncol ? first + (c0 + col) / G : -1;
+      low[n][e] = win ? max(0, pos[n][e] - p.window + 1) : 0;
+      cs[n][e] = qscale[col];
+      m[n][e] = -INFINITY;
+      mref[n][e] = l[n][e] = 0.f;
+      A[n][e] = -INFINITY;
+      F[n][e] = 0.f;
+      thr[n][e] = kTiny;
+    }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
+
+  bool ok = true;
+  for (int it = 0; it < mine; ++it) {
+    const int slot = it % C::kStages;
+    if (!__all_sync(0xFFFFFFFFu, bar_wait(&bars[slot], (it / C::kStages) & 1) ? 1 : 0)) {
+      ok = false;
+      // let the copies still in flight land before the ring is reused
+      for (int j = it; j < min(mine, it + C::kStages); ++j)
+        if (!bar_wait(&bars[j % C::kStages], (j / C::kStages) & 1)) break;
+      break;
+    }
+    const bool have = (good >> slot) & 1u;
+    const int j0 = unit_at(it) * C::kKeys;
+    const uint8_t* Ks = ring + (size_t)slot * C::kStage;
+    const uint8_t* Vs = Ks + C::kHalf;
+    if (have) {
+      // ---- scores: S[key][col]; block bt: keys key_of(bt)
+      float sc[NT][KB / 2][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < KB / 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[n][i][e] = 0.f;
+      // position in the page of this lane's key of block bt
+      auto key_of = [&](int bt) { return FMT ? 8 * (lg >> 1) + 2 * bt + (lg & 1) : 8 * bt + lg; };
+      if constexpr (FMT == 1) {
+        uint32_t kw[KB][D / 32], ks[KB];
+#pragma unroll
+        for (int bt = 0; bt < KB; ++bt) {
+          const int r = key_of(bt);
+          if constexpr (D == 128) {
+            *reinterpret_cast<uint4*>(kw[bt]) = *reinterpret_cast<const uint4*>(Ks + r * 64 + lt * 16);
+            ks[bt] = e4m3x2_f16(*reinterpret_cast<const uint16_t*>(Ks + Kv4<D>::kCodes + r * 8 + 2 * lt));
+          } else {
+            *reinterpret_cast<uint2*>(kw[bt]) = *reinterpret_cast<const uint2*>(Ks + r * 32 + lt * 8);
+            ks[bt] = e4m3x2_f16(Ks[Kv4<D>::kCodes + r * 4 + lt]);
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          uint32_t a[KB][4];
+#pragma unroll
+          for (int bt = 0; bt < KB; ++bt) {
+            const uint32_t s2 = __byte_perm(ks[bt], 0, w < 2 ? 0x1010 : 0x3232);
+            e2m1x8(kw[bt][w], a[bt]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[bt][i] = hmul2u(a[bt][i], s2);
+          }
+#pragma unroll
+          for (int st = 0; st < 2; ++st)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int q = 0; q < C::kQp; ++q) {
+                const uint2 bq = qf[((n * C::kQp + q) * C::kSteps + 2 * w + st) * 32];
+#pragma unroll
+                for (int i = 0; i < KB / 2; ++i)
+                  mma16816<1>(sc[n][i], a[2 * i][2 * st], a[2 * i + 1][2 * st], a[2 * i][2 * st + 1],
+                              a[2 * i + 1][2 * st + 1], bq.x, bq.y);
+              }
+        }
+      } else {
+        const uint32_t kb = smem_u32(Ks);
+        const int r = (lane & 7) + ((lane >> 3) & 1) * 8, ch = lane >> 4;
+#pragma unroll
+        for (int s = 0; s < C::kSteps; ++s) {
+          uint32_t a[4];
+          const int cc = 2 * s + ch;
+          ldsm4(a, kb + (cc >> 3) * (16 * 128) + r * 128 + (((cc & 7) ^ (r & 7)) << 4));
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int q = 0; q < C::kQp; ++q) {
+              const uint2 bq = qf[((n * C::kQp + q) * C::kSteps + s) * 32];
+              mma16816<0>(sc[n][0], a[0], a[1], a[2], a[3], bq.x, bq.y);
+            }
+        }
+      }
+
+      // Does every column see every key of the stage?  Else: mask, and keep what no column sees (and
+      // infinities and NaN that only some see) out of the second product.
+      const int j1 = j0 + C::kKeys - 1;
+      const bool whole = j1 <= posmin && (j0 >= lowmax || j1 < sinks);
+      uint32_t dead = 0, poison = 0;  // bits: positions of the stage
+      if (!whole) {
+        const int j = j0 + (lane & (C::kKeys - 1));
+        const bool any = j <= posmax && (j >= lowmin || j < sinks);
+        dead = __ballot_sync(0xFFFFFFFFu, !any);
+        if constexpr (FMT == 1) {
+          const int blk = D == 128 ? lg : lg >> 1;
+          const uint2 w = *reinterpret_cast<const uint2*>(Vs + Kv4<D>::kCodes + blk * kKvPage + 8 * lt);
+          uint32_t bad = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) bad |= ((((i < 4 ? w.x : w.y) >> (8 * (i & 3))) & 0x7Fu) == 0x7Fu ? 1u : 0u) << i;
+          poison = __reduce_or_sync(0xFFFFFFFFu, bad << (8 * lt)) & ~dead;
+        } else {
+          uint32_t bad = 0;
+          const uint32_t vb = smem_u32(Vs);
+          const int r = (lane & 7) + ((lane >> 4) & 1) * 8, ch = (lane >> 3) & 1;
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            uint32_t a[4];
+            const int cc = 2 * i + ch;
+            ldsm4t(a, vb + (cc >> 3) * (16 * 128) + r * 128 + (((cc & 7) ^ (r & 7)) << 4));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int k = (e >> 1) * 8 + 2 * lt;
+              bad |= ((a[e] & 0x7F80u) == 0x7F80u ? 1u : 0u) << k;
+              bad |= ((a[e] & 0x7F800000u) == 0x7F800000u ? 2u : 0u) << k;
+            }
+          }
+          poison = __reduce_or_sync(0xFFFFFFFFu, bad) & ~dead;
+        }
+        dead |= poison;
+      }
+
+      // ---- softmax
+      float kscale[KB], vscale[KB];
+#pragma unroll
+      for (int bt = 0; bt < KB; ++bt) {
+        kscale[bt] = FMT ? reinterpret_cast<const float*>(Ks + Kv4<D>::kRows)[key_of(bt)] : 1.f;
+        vscale[bt] = FMT ? reinterpret_cast<const float*>(Vs + Kv4<D>::kRows)[key_of(bt)] : 1.f;
+      }
+      float z[NT][KB][2];
+      bool grow = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int bt = 0; bt < KB; ++bt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float t = sc[n][bt >> 1][(bt & 1) * 2 + e] * cs[n][e];
+            if constexpr (FMT == 1) t *= kscale[bt];
+            if (!whole) {
+              const int j = j0 + key_of(bt);
+              if (!(j <= pos[n][e] && (j >= low[n][e] || j < sinks))) t = -INFINITY;
+            }
+            z[n][bt][e] = t;
+            grow |= t > m[n][e] + kGrow;
+          }
+      if (__any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = z[n][0][e];
+#pragma unroll
+            for (int bt = 1; bt < KB; ++bt) mx = fmaxf(mx, z[n][bt][e]);
+#pragma unroll
+            for (int s = 4; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, s));
+            if (mx > m[n][e] + kGrow) {
+              const float f = m[n][e] == -INFINITY ? 0.f : ex2f(m[n][e] - mx);
+              l[n][e] *= f;
+              m[n][e] = mref[n][e] = mx;
+              if constexpr (FMT == 0) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                  o[n][i][e] *= f;
+                  o[n][i][2 + e] *= f;
+                }
+              } else if (A[n][e] != -INFINITY) {
+                if (mx - A[n][e] <= 120.f) {
+                  F[n][e] = ex2f(mx - A[n][e]);
+                  thr[n][e] = ex2f(A[n][e] - mx + kRefTop);
+                } else {  // nothing is left of the outputs so far
+#pragma unroll
+                  for (int i = 0; i < MT; ++i) o[n][i][e] = o[n][i][2 + e] = 0.f;
+                  A[n][e] = -INFINITY;
+                  F[n][e] = 0.f;
+                  thr[n][e] = kTiny;
+                }
+              }
+            }
+          }
+      }
+      bool wide = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int bt = 0; bt < KB; ++bt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float pr = ex2f(z[n][bt][e] - mref[n][e]);
+            if (poison && ((poison >> key_of(bt)) & 1u) && z[n][bt][e] != -INFINITY) pr = __int_as_float(0x7FFFFFFF);
+            l[n][e] += pr;
+            if constexpr (FMT == 1) {
+              // a masked position's row scale may be anything
+              pr = (!whole && z[n][bt][e] == -INFINITY) ? 0.f : pr * vscale[bt];
+              wide |= pr > thr[n][e];
+            }
+            z[n][bt][e] = pr;
+          }
+      // FMT 1: the outputs' reference A (log2): they are kept divided by 2^A, so that the f16 parts of
+      // p * (V's row scale) / 2^A keep their bits whatever the size of the rows: each is off by 2^-23 of
+      // itself (two parts) or by 2^-25, half of f16's smallest step, i.e. 2^-32 of the largest weight.
+      if (FMT == 1 && __any_sync(0xFFFFFFFFu, wide)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = z[n][0][e];
+#pragma unroll
+            for (int bt = 1; bt < KB; ++bt) mx = fmaxf(mx, z[n][bt][e]);
+#pragma unroll
+            for (int s = 4; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, s));
+            if (mx > thr[n][e]) {
+              const float An = mref[n][e] + lg2f(mx) - kRefBits;
+              const float f = A[n][e] == -INFINITY ? 0.f : ex2f(A[n][e] - An);
+#pragma unroll
+              for (int i = 0; i < MT; ++i) {
+                o[n][i][e] *= f;
+                o[n][i][2 + e] *= f;
+              }
+              A[n][e] = An;
+              F[n][e] = ex2f(mref[n][e] - An);
+              thr[n][e] = ex2f(An - mref[n][e] + kRefTop);
+            }
+          }
+      }
+      // ---- probabilities as the second product's column operand: block bt holds (key, column) pairs as the
+      // first product left them; the transpose gives (column, key pair)
+      uint32_t pb[NT][C::kPp][KB];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int bt = 0; bt < KB; ++bt) {
+          uint32_t part[C::kPp];
+          if constexpr (FMT == 1)
+            split_pair<1, C::kPp>(z[n][bt][0] * F[n][0], z[n][bt][1] * F[n][1], part);
+          else
+            split_pair<0, C::kPp>(z[n][bt][0], z[n][bt][1], part);
+#pragma unroll
+          for (int q = 0; q < C::kPp; ++q) pb[n][q][bt] = movmatrix(part[q]);
+        }
+      // ---- O^T += V^T P^T
+      if constexpr (FMT == 1) {
+        uint32_t vw[KB][D / 32], vs[KB];
+        const int blk = D == 128 ? lg : lg >> 1;
+        uint2 w8 = *reinterpret_cast<const uint2*>(Vs + Kv4<D>::kCodes + blk * kKvPage + 8 * lt);
+        if (dead) {  // zero the scales of positions that must not enter
+          const uint32_t d8 = dead >> (8 * lt);
+          uint32_t keep[2] = {0, 0};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) keep[i >> 2] |= ((d8 >> i) & 1u ? 0u : 0xFFu) << (8 * (i & 3));
+          w8.x &= keep[0];
+          w8.y &= keep[1];
+        }
+        vs[0] = e4m3x2_f16(w8.x & 0xFFFFu);
+        vs[1] = e4m3x2_f16(w8.x >> 16);
+        vs[2] = e4m3x2_f16(w8.y & 0xFFFFu);
+        vs[3] = e4m3x2_f16(w8.y >> 16);
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+          if constexpr (D == 128)
+            *reinterpret_cast<uint4*>(vw[j]) = *reinterpret_cast<const uint4*>(Vs + j * 512 + lane * 16);
+          else
+            *reinterpret_cast<uint2*>(vw[j]) =
+                *reinterpret_cast<const uint2*>(Vs + j * 256 + (lg >> 1) * 64 + lt * 16 + (lg & 1) * 8);
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          uint32_t a[KB][4];
+#pragma unroll
+          for (int j = 0; j < KB; ++j) {
+            e2m1x8(vw[j][w], a[j]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[j][i] = hmul2u(a[j][i], vs[j]);
+          }
+#pragma unroll
+          for (int st = 0; st < 2; ++st)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int q = 0; q < C::kPp; ++q)
+#pragma unroll
+                for (int i = 0; i < KB / 2; ++i)
+                  mma16816<1>(o[n][2 * w + st], a[2 * i][2 * st], a[2 * i][2 * st + 1], a[2 * i + 1][2 * st],
+                              a[2 * i + 1][2 * st + 1], pb[n][q][2 * i], pb[n][q][2 * i + 1]);
+        }
+      } else {
+        const uint32_t vb = smem_u32(Vs);
+        const int r = (lane & 7) + ((lane >> 4) & 1) * 8, ch = (lane >> 3) & 1;
+        const uint32_t dl = dead >> (2 * lt);
+        const uint32_t keep0 = ((dl & 1u) ? 0u : 0xFFFFu) | ((dl & 2u) ? 0u : 0xFFFF0000u);
+        const uint32_t keep1 = ((dl & 0x100u) ? 0u : 0xFFFFu) | ((dl & 0x200u) ? 0u : 0xFFFF0000u);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          uint32_t a[4];
+          const int cc = 2 * i + ch;
+          ldsm4t(a, vb + (cc >> 3) * (16 * 128) + r * 128 + (((cc & 7) ^ (r & 7)) << 4));
+          if (dead) {
+            a[0] &= keep0;
+            a[1] &= keep0;
+            a[2] &= keep1;
+            a[3] &= keep1;
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int q = 0; q < C::kPp; ++q)
+              mma16816<0>(o[n][i], a[0], a[1], a[2], a[3], pb[n][q][0], pb[n][q][1]);
+        }
+      }
+    }
+    __syncwarp();
+    if (it + C::kStages < mine) {
+      const int pg = issue(it + C::kStages);
+      good = (good & ~(1u << slot)) | ((pg >= 0 ? 1u : 0u) << slot);
+    }
+  }
+  if (!ok && lane == 0) cache_flag(c, TF_CACHE_TIMEOUT);
+
+  // ---- the warps' partials meet in shared memory (over the ring: every copy has landed and been read)
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int s = 4; s < 32; s <<= 1) l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], s);
+  __syncthreads();
+  float* wpart = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int col = n * 8 + 2 * lt + e;
+      float* wp = wpart + ((size_t)warp * C::kCols + col) * C::kLd;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        if constexpr (FMT == 1) {
+          *reinterpret_cast<float2*>(wp + lg * (D / 8) + 2 * i) = make_float2(o[n][i][e], o[n][i][2 + e]);
+        } else {
+          wp[16 * i + lg] = o[n][i][e];
+          wp[16 * i + 8 + lg] = o[n][i][2 + e];
+        }
+      }
+      if (lg == 0) {
+        wref[warp * C::kCols + col] = FMT ? A[n][e] : m[n][e];
+        wmax[warp * C::kCols + col] = m[n][e];
+        wsum[warp * C::kCols + col] = l[n][e];
+      }
+    }
+  __syncthreads();
+  if (threadIdx.x < C::kCols) {
+    const int col = threadIdx.x;
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int w = 0; w < C::kWarps; ++w) M = fmaxf(M, wmax[w * C::kCols + col]);
+#pragma unroll
+    for (int w = 0; w < C::kWarps; ++w) {
+      const float mw = wmax[w * C::kCols + col], rw = wref[w * C::kCols + col], lw = wsum[w * C::kCols + col];
+      L += mw == -INFINITY ? lw : lw * ex2f(mw - M);             // lw: 0, or NaN
+      wref[w * C::kCols + col] = rw == -INFINITY ? 0.f : ex2f(rw - M);  // the factor of the warp's outputs
+    }
+    cmax[col] = M;
+    csum[col] = L;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < ncol * D; e += 256) {
+    const int col = e / D, d = e - col * D;
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < C::kWarps; ++w) {
+      const float f = wref[w * C::kCols + col];
+      if (f != 0.f) s = fmaf(wpart[((size_t)w * C::kCols + col) * C::kLd + d], f, s);
+    }
+    cpart[e] = s;
+  }
+  // ---- the CTAs of the cluster: each finishes its share of the outputs, adding the ranks in order
+  auto cluster_sync = [&]() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  };
+  if (csize > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  auto peer = [&](const float* a, int r) {
+    if (csize == 1) return *a;
+    uint32_t ra;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(smem_u32(a)), "r"(r));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(ra) : "memory");
+    return v;
+  };
+  const int share = (ncol * D + csize - 1) / csize;
+  for (int e = rank * share + threadIdx.x; e < min(ncol * D, (rank + 1) * share); e += 256) {
+    const int col = e / D, d = e - col * D;
+    float M = -INFINITY, L = 0.f, s = 0.f;
+    for (int r = 0; r < csize; ++r) M = fmaxf(M, peer(cmax + col, r));
+    for (int r = 0; r < csize; ++r) {
+      const float mr = peer(cmax + col, r), lr = peer(csum + col, r);
+      const float f = mr == -INFINITY ? 1.f : ex2f(mr - M);
+      L = fmaf(lr, f, L);
+      if (mr != -INFINITY) s = fmaf(peer(cpart + e, r), f, s);
+    }
+    const float y = L == 0.f ? 0.f : s / L;
+    const int cc = c0 + col;
+    const size_t oo = (size_t)(sq.r0 + cc / G) * p.out_stride + (size_t)(hkv * G + cc % G) * D + d;
+    if (F32)
+      static_cast<float*>(p.out)[oo] = y;
+    else
+      static_cast<uint16_t*>(p.out)[oo] = f32_to_bf16(y);
+  }
+  if (csize > 1) cluster_sync();  // nobody leaves while a peer may read its shared memory
+}
+
+template <int D, int FMT, int NT, int F32>
+cudaError_t launch_decode_t(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnParams& p,
+                            cudaStream_t s) {
+  using C = DecCfg<D, FMT, NT, F32>;
+  static DeviceOnce once;
+  cudaError_t e = device_once(once, [] {
+    cudaError_t r = cudaFuncSetAttribute(k_cache_decode<D, FMT, NT, F32>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    if (r) return r;
+    return cudaFuncSetAttribute(k_cache_decode<D, FMT, NT, F32>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  });
+  if (e) return e;
+  const int G = p.Hq / p.c.Hkv;
+  const int64_t tiles = ((int64_t)p.c.max_rows * G + C::kCols - 1) / C::kCols;
+  // CTAs per group: enough to give every SM two, as long as a warp still gets a stage.
+  const int64_t keys = p.window > 0 ? std::min<int64_t>(p.c.max_len, (int64_t)p.window + p.sinks + 8) : p.c.max_len;
+  const int64_t groups = tiles * p.c.Hkv * p.c.n_seq;
+  int cs = 1;
+  while (cs < 16 && groups * cs < 2 * 152 && (int64_t)cs * C::kWarps * C::kKeys < keys) cs *= 2;
+  if (tiles * cs > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * cs), p.c.Hkv, p.c.n_seq);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cs;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_cache_decode<D, FMT, NT, F32>, mk, mv, p, cs);
+}
+
+template <int D, int FMT, int F32>
+cudaError_t launch_decode_n(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnParams& p,
+                            cudaStream_t s) {
+  const int64_t cols = (int64_t)p.c.max_rows * (p.Hq / p.c.Hkv);
+  if (cols <= 8) return launch_decode_t<D, FMT, 1, F32>(mk, mv, p, s);
+  if (cols <= 16) return launch_decode_t<D, FMT, 2, F32>(mk, mv, p, s);
+  return launch_decode_t<D, FMT, 4, F32>(mk, mv, p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_decode(const CacheAttnParams& p, cudaStream_t s) {
+  CUtensorMap mk = {}, mv = {};
+  if (p.c.fmt == 0) {
+    const uint64_t rows = (uint64_t)p.c.n_pages * p.c.Hkv * kKvPage;
+    if (!make_map(&mk, p.c.K, rows, p.c.D, 16) || !make_map(&mv, p.c.V, rows, p.c.D, 16))
+      return cudaErrorInvalidValue;
+  }
+#define TF_DEC(DV)                                                                                  \
+  (p.c.fmt ? (p.f32 ? launch_decode_n<DV, 1, 1>(mk, mv, p, s) : launch_decode_n<DV, 1, 0>(mk, mv, p, s)) \
+           : (p.f32 ? launch_decode_n<DV, 0, 1>(mk, mv, p, s) : launch_decode_n<DV, 0, 0>(mk, mv, p, s)))
+  return p.c.D == 128 ? TF_DEC(128) : TF_DEC(64);
+#undef TF_DEC
+}
+
+}  // namespace tf

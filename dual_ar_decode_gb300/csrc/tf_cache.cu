@@ -20,7 +20,7 @@ bool batch_of(const tf_kv_cache* c, CacheBatch* b) {
       c->n_seq > 65535 || c->n_rows < 0 || c->max_rows < 0 || c->max_length < 0)
     return false;
   if ((int64_t)c->n_pages * c->n_kv_heads * kKvPage >= (1ll << 31)) return false;
-  if (c->table_stride > (1 << 26) || (int64_t)c->max_rows * c->n_kv_heads >= (1ll << 31)) return false;
+  if (c->table_stride > (1 << 25) || c->n_rows >= (1 << 27) || (int64_t)c->max_rows * c->n_kv_heads >= (1ll << 31)) return false;
   if (!aligned(c->K, 128) || !aligned(c->V, 128) || !aligned(c->block_table, 4) || !aligned(c->lengths, 4) ||
       !aligned(c->row_start, 4) || !aligned(c->err, 4))
     return false;
@@ -89,11 +89,12 @@ tf_status tf_op_attention_cache(const tf_kv_cache* cache, const void* q, int64_t
   p.out_stride = out_stride ? out_stride : row;
   p.f32 = dtype == TF_DTYPE_F32;
   p.Hq = n_heads;
-  p.window = window;
-  p.sinks = sinks;
+  // positions are below 2^30: a wider window or more sinks change nothing
+  p.window = window < (1 << 30) ? window : 1 << 30;
+  p.sinks = sinks < (1 << 30) ? sinks : 1 << 30;
   const double sc = scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)p.c.D);
   p.scale_log2 = static_cast<float>(sc * 1.4426950408889634);
-  return launch_cache_attention(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TF_OK : TF_E_CUDA;
+  return launch_cache_decode(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TF_OK : TF_E_CUDA;
 }
 
 tf_status tf_op_cache_append(const tf_kv_cache* cache, const void* k, const void* v, int64_t stride,

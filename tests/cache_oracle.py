@@ -114,12 +114,12 @@ class Pool:
 
 
 def attention(q, k, v, n, window=0, sinks=0, scale=None, hidden=None):
-    """q float64 [r, Hq, D], the last r of n positions; k, v float64 [n, Hkv, D] -> out, sum p|v| (the same shape)
-    and per (row, head) the largest scale * sum |q||k| over what the row sees."""
+    """q float64 [r, Hq, D], the last r of n positions; k, v float64 [n, Hkv, D] -> out, sum p|v| (the same shape),
+    per (row, head) the largest scale * sum |q||k| over what the row sees, and the largest p_j max|v_j|."""
     r, Hq, D = q.shape
     Hkv = k.shape[1]
     scale = scale or D ** -0.5
-    out, mass, reach = np.zeros_like(q), np.zeros_like(q), np.zeros((r, Hq))
+    out, mass, reach, peak = np.zeros_like(q), np.zeros_like(q), np.zeros((r, Hq)), np.zeros((r, Hq))
     for i in range(r):
         p = n - r + i
         j = np.arange(n)
@@ -137,17 +137,22 @@ def attention(q, k, v, n, window=0, sinks=0, scale=None, hidden=None):
             w /= w.sum()
             out[i, h], mass[i, h] = w @ v[see, g], w @ np.abs(v[see, g])
             reach[i, h] = (np.abs(k[see, g]) @ np.abs(q[i, h])).max() * scale
-    return out, mass, reach
+            peak[i, h] = (w * np.abs(v[see, g]).max(-1)).max()
+    return out, mass, reach, peak
 
 
-def tolerance(out, mass, reach, D, n, dtype):
+def tolerance(out, mass, reach, peak, D, n, dtype, fmt):
     """How far an output may be.  A score is a float32 sum of D products of exact keys with queries of 22 or more
     bits: off by at most d = (D + 8) 2^-24 reach (+ 2^-22 reach for the queries' bits).  A probability's relative
     error is then 2 d plus the exponential's 2^-20; numerator and denominator each carry it and the n + 64 additions
-    of a float32 sum (2^-24 each, against the sum of p|v|).  bf16 rows: the probabilities' rounding to bf16 (half a
-    step: 2^-8 of each) and the output's (2^-8 of it)."""
+    of a float32 sum (2^-24 each, against the sum of p|v|).  4-bit pages: a weight p * (row scale) enters as f16
+    parts whose smallest step is 2^-24 where the largest weight is at least 2^7: each of n weights is off by at most
+    2^-25 / 2^7 of the largest one, and its element is at most its row's largest.  bf16 rows: the probabilities'
+    rounding to bf16 (half a step: 2^-8 of each) and the output's (2^-8 of it)."""
     d = ((D + 8) * 2.0 ** -24 + 2.0 ** -22) * reach[..., None]
     t = (2 * (2 * d + 2.0 ** -20) + 2 * (n + 64) * 2.0 ** -24) * mass
+    if fmt == "nvfp4":
+        t = t + n * 2.0 ** -32 * peak[..., None]
     if dtype == "bf16":
         t = t + 2.0 ** -8 * mass + 2.0 ** -8 * (np.abs(out) + t)
     return t + 1e-30

@@ -68,9 +68,9 @@ def check(batch, q, out, Hq, dtype, window=0, sinks=0, scale=None, hidden=None, 
     for b, r in enumerate(batch.counts):
         n = int(lens[b])
         qb = qn[row:row + r, :Hq * D].reshape(r, Hq, D)
-        want, mass, reach = attention(qb, pool.k[b][:n], pool.v[b][:n], n, window, sinks, scale,
+        want, *sizes = attention(qb, pool.k[b][:n], pool.v[b][:n], n, window, sinks, scale,
                                       None if hidden is None else hidden[b][:n])
-        tol = tolerance(want, mass, reach, D, n, dtype)
+        tol = tolerance(want, *sizes, D, n, dtype, pool.fmt)
         diff = np.abs(got[row:row + r, :Hq * D].reshape(r, Hq, D) - want)
         assert np.all(diff <= tol), (b, n, r, float((diff / tol).max()), float(diff.max()))
         row += r
