@@ -173,7 +173,7 @@ struct DecCfg {
   static constexpr int kKeys = FMT ? 32 : 16;               // positions of a stage (a page, or half a page)
   static constexpr int kHalf = FMT ? Kv4<D>::kBytes : 16 * D * 2;  // K (or V) bytes of a stage
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = FMT ? 2 : (D == 64 ? 4 : NT == 4 ? 2 : 3);
+  static constexpr int kStages = FMT ? 2 : (D == 64 ? 4 : NT == 3 ? 2 : 3);
   static constexpr int kQp = FMT ? (F32 ? 2 : 1) : (F32 ? 3 : 1);  // parts of a query
   static constexpr int kPp = FMT ? (F32 ? 2 : 1) : (F32 ? 3 : 2);  // parts of a probability
   static constexpr int kSteps = D / 16;
@@ -721,50 +721,105 @@ __global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
     csum[col] = L;
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < ncol * D; e += 256) {
-    const int col = e / D, d = e - col * D;
-    float s = 0.f;
+  const int quads = ncol * (D / 4);  // 4 dims of a column each
+  for (int e = threadIdx.x; e < quads; e += 256) {
+    const int col = e / (D / 4), d = e % (D / 4) * 4;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < C::kWarps; ++w) {
       const float f = wref[w * C::kCols + col];
-      if (f != 0.f) s = fmaf(wpart[((size_t)w * C::kCols + col) * C::kLd + d], f, s);
+      if (f != 0.f) {
+        const float4 v = *reinterpret_cast<const float4*>(wpart + ((size_t)w * C::kCols + col) * C::kLd + d);
+        s.x = fmaf(v.x, f, s.x);
+        s.y = fmaf(v.y, f, s.y);
+        s.z = fmaf(v.z, f, s.z);
+        s.w = fmaf(v.w, f, s.w);
+      }
     }
-    cpart[e] = s;
+    *reinterpret_cast<float4*>(cpart + (size_t)e * 4) = s;
   }
   // ---- the CTAs of the cluster: each finishes its share of the outputs, adding the ranks in order
   auto cluster_sync = [&]() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   };
-  if (csize > 1)
-    cluster_sync();
-  else
-    __syncthreads();
-  auto peer = [&](const float* a, int r) {
-    if (csize == 1) return *a;
+  auto peer = [&](const void* a, int r) {
     uint32_t ra;
-    float v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(smem_u32(a)), "r"(r));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(ra) : "memory");
-    return v;
+    return ra;
   };
-  const int share = (ncol * D + csize - 1) / csize;
-  for (int e = rank * share + threadIdx.x; e < min(ncol * D, (rank + 1) * share); e += 256) {
-    const int col = e / D, d = e - col * D;
-    float M = -INFINITY, L = 0.f, s = 0.f;
-    for (int r = 0; r < csize; ++r) M = fmaxf(M, peer(cmax + col, r));
-    for (int r = 0; r < csize; ++r) {
-      const float mr = peer(cmax + col, r), lr = peer(csum + col, r);
-      const float f = mr == -INFINITY ? 1.f : ex2f(mr - M);
-      L = fmaf(lr, f, L);
-      if (mr != -INFINITY) s = fmaf(peer(cpart + e, r), f, s);
+  float* fac = wmax;    // [rank][col]: factor of a rank's outputs (16 ranks: over wmax and wsum)
+  float* total = qscale;
+  if (csize > 1) {
+    cluster_sync();
+    for (int e = threadIdx.x; e < csize * C::kCols; e += 256) {
+      float v;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer(cmax + e % C::kCols, e / C::kCols)) : "memory");
+      fac[e] = v;
     }
-    const float y = L == 0.f ? 0.f : s / L;
+    __syncthreads();
+    if (threadIdx.x < C::kCols) {
+      const int col = threadIdx.x;
+      float M = -INFINITY, L = 0.f;
+      for (int r = 0; r < csize; ++r) M = fmaxf(M, fac[r * C::kCols + col]);
+      for (int r = 0; r < csize; ++r) {
+        float lr;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(lr) : "r"(peer(csum + col, r)) : "memory");
+        const float mr = fac[r * C::kCols + col];
+        const float f = mr == -INFINITY ? 0.f : ex2f(mr - M);
+        fac[r * C::kCols + col] = f;
+        L += mr == -INFINITY ? lr : lr * f;  // lr: 0, or NaN
+      }
+      total[col] = L;
+    }
+    __syncthreads();
+  } else {
+    if (threadIdx.x < C::kCols) total[threadIdx.x] = csum[threadIdx.x];
+    __syncthreads();
+  }
+  const int share = (quads + csize - 1) / csize;
+  for (int e = rank * share + threadIdx.x; e < min(quads, (rank + 1) * share); e += 256) {
+    const int col = e / (D / 4), d = e % (D / 4) * 4;
+    float y[4] = {0.f, 0.f, 0.f, 0.f};
+    if (csize > 1) {
+#pragma unroll 4
+      for (int r = 0; r < csize; ++r) {
+        const float f = fac[r * C::kCols + col];
+        float4 v;
+        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                     : "r"(peer(cpart + (size_t)e * 4, r))
+                     : "memory");
+        if (f != 0.f) {
+          y[0] = fmaf(v.x, f, y[0]);
+          y[1] = fmaf(v.y, f, y[1]);
+          y[2] = fmaf(v.z, f, y[2]);
+          y[3] = fmaf(v.w, f, y[3]);
+        }
+      }
+    } else {
+      *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(cpart + (size_t)e * 4);
+    }
+    const float L = total[col], inv = L == 0.f ? 0.f : 1.f / L;
     const int cc = c0 + col;
     const size_t oo = (size_t)(sq.r0 + cc / G) * p.out_stride + (size_t)(hkv * G + cc % G) * D + d;
-    if (F32)
-      static_cast<float*>(p.out)[oo] = y;
-    else
-      static_cast<uint16_t*>(p.out)[oo] = f32_to_bf16(y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = L == 0.f ? 0.f : y[i] * inv;
+    if constexpr (F32) {
+      float* o4 = static_cast<float*>(p.out) + oo;
+      if ((reinterpret_cast<uintptr_t>(o4) & 15) == 0)
+        *reinterpret_cast<float4*>(o4) = make_float4(y[0], y[1], y[2], y[3]);
+      else
+        for (int i = 0; i < 4; ++i) o4[i] = y[i];
+    } else {
+      uint16_t* o4 = static_cast<uint16_t*>(p.out) + oo;
+      uint16_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = f32_to_bf16(y[i]);
+      if ((reinterpret_cast<uintptr_t>(o4) & 7) == 0)
+        *reinterpret_cast<uint2*>(o4) = make_uint2(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16);
+      else
+        for (int i = 0; i < 4; ++i) o4[i] = w[i];
+    }
   }
   if (csize > 1) cluster_sync();  // nobody leaves while a peer may read its shared memory
 }
@@ -810,7 +865,7 @@ cudaError_t launch_decode_n(const CUtensorMap& mk, const CUtensorMap& mv, const 
   const int64_t cols = (int64_t)p.c.max_rows * (p.Hq / p.c.Hkv);
   if (cols <= 8) return launch_decode_t<D, FMT, 1, F32>(mk, mv, p, s);
   if (cols <= 16) return launch_decode_t<D, FMT, 2, F32>(mk, mv, p, s);
-  return launch_decode_t<D, FMT, 4, F32>(mk, mv, p, s);
+  return launch_decode_t<D, FMT, 3, F32>(mk, mv, p, s);
 }
 
 }  // namespace
