@@ -17,7 +17,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libtf_dualar.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["tf_api.cu", "kernels_gemv.cu", "kernels_attn.cu", "kernels_misc.cu", "kernels_umma.cu",
-           "kernels_cache.cu", "kernels_cache_attn.cu", "tf_cache.cu"]
+           "kernels_cache.cu", "kernels_cache_attn.cu", "kernels_cache_prompt.cu",
+           "tf_cache.cu"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC", "-Xcompiler", "-O2", "--expt-relaxed-constexpr",

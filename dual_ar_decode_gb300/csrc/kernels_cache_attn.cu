@@ -47,6 +47,7 @@ namespace tf {
 
 namespace {
 
+constexpr int kSortMax = 256;  // sequences that a CTA puts in order of length
 constexpr float kGrow = 8.0f;  // log2 of the growth at which a reference is replaced
 // 4-bit pages: the weights p * (V's row scale) are multiplied in f16 parts, relative to a reference 2^A
 // that puts the largest at 2^7 when it is set and lets it grow to 2^15.
@@ -91,13 +92,13 @@ template <int FMT>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
   if constexpr (FMT == 0)
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -106,20 +107,18 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
 }
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
 }
 
 // Four bytes of e2m1 pairs -> four f16x2 (low nibble in the low half).
@@ -178,14 +177,19 @@ struct DecCfg {
   static constexpr int kPp = FMT ? (F32 ? 2 : 1) : (F32 ? 3 : 2);  // parts of a probability
   static constexpr int kSteps = D / 16;
   static constexpr int kCols = 8 * NT;
-  static constexpr int kLd = D + 8;                         // row of a warp's partial outputs
+  // A warp's partial outputs.  FMT 0: [col][kLd]; FMT 1: float2 (two dims of a lane) [n-tile][16-row tile]
+  // [kPair: col * 10 + lane group]; both strides keep the stores and the reads free of bank conflicts.
+  static constexpr int kLd = D + 4, kPair = 82;
+  static constexpr int kPartFloats = FMT ? NT * kSteps * kPair * 2 : kCols * kLd;
+  static constexpr int kMaxRanks = 16;
   static constexpr size_t kRing = (size_t)kWarps * kStages * kStage;
-  static constexpr size_t kParts = (size_t)kWarps * kCols * kLd * 4;  // overlays the ring at the end
+  static constexpr size_t kParts = (size_t)kWarps * kPartFloats * 4;  // overlays the ring at the end
   static constexpr size_t kOffQ = ((kRing > kParts ? kRing : kParts) + 127) / 128 * 128;
-  static constexpr size_t kOffC = kOffQ + (size_t)NT * kQp * kSteps * 32 * 8;  // the CTA's partial [kCols][D]
-  static constexpr size_t kOffStat = kOffC + (size_t)kCols * D * 4;
-  // per warp and column: reference of the outputs, maximum, sum; per column: the CTA's maximum and sum; scale
-  static constexpr size_t kOffBar = kOffStat + (size_t)(3 * kWarps + 3) * kCols * 4;
+  // what the cluster's ranks send to this CTA: [rank][its share of the outputs], [rank][col] maxima and sums
+  static constexpr size_t kOffC = kOffQ + (size_t)NT * kQp * kSteps * 32 * 8;
+  static constexpr size_t kOffStat = kOffC + (size_t)(kCols * D / 4 + kMaxRanks) * 16 + 2 * kMaxRanks * kCols * 4;
+  // per warp and column: reference of the outputs, maximum, sum; per column: the queries' scale
+  static constexpr size_t kOffBar = kOffStat + (size_t)(3 * kWarps + 1) * kCols * 4;
   static constexpr size_t kSmem = 1024 + kOffBar + kWarps * kStages * 8 + 16;
 };
 
@@ -197,7 +201,7 @@ struct TileRows {
 template <int D, int FMT, int NT, int F32>
 __global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
     k_cache_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                   const CacheAttnParams p, const int csize) {
+                   const CacheAttnParams p, const int csize, const int sorted) {
   using C = DecCfg<D, FMT, NT, F32>;
   constexpr int KB = C::kKeys / 8;   // blocks of 8 keys in a stage
   constexpr int MT = D / 16;         // 16-row tiles of the head dimension
@@ -207,12 +211,31 @@ __global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
   const CacheBatch& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = lane >> 2, lt = lane & 3;
   const int rank = static_cast<int>(blockIdx.x) % csize, tile = static_cast<int>(blockIdx.x) / csize;
-  const int hkv = blockIdx.y, b = blockIdx.z;
+  const int hkv = blockIdx.y;
   const int G = p.Hq / c.Hkv;
+  // Ragged batches of more CTAs than fit at once: the longest sequences first, so that the last CTAs to
+  // start are short ones.
+  int b = blockIdx.z;
+  if (sorted) {
+    __shared__ int lens[kSortMax], chosen;
+    const int t = threadIdx.x, n = c.n_seq;
+    const int mine = t < n ? __ldg(c.len + t) : 0;
+    if (t < n) lens[t] = mine;
+    __syncthreads();
+    if (t < n) {
+      int r = 0;
+      for (int i = 0; i < n; ++i) r += (lens[i] > mine || (lens[i] == mine && i < t)) ? 1 : 0;
+      if (r == b) chosen = t;
+    }
+    __syncthreads();
+    b = chosen;
+  }
   const SeqRows sq = cache_seq(c, b);
   const int c0 = tile * C::kCols;
   const int ncol = min(C::kCols, sq.n * G - c0);
   if (ncol <= 0) return;  // the whole cluster
+  // (waited for before the first store to a peer's shared memory: it must have started)
+  if (csize > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int first = sq.len - sq.n;                       // position of the sequence's row 0
   const int posmin = first + c0 / G, posmax = first + (c0 + ncol - 1) / G;
   const bool win = p.window > 0;
@@ -225,13 +248,13 @@ __global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
   const int usink = min(ulow, (min(sinks, lowmin) + C::kKeys - 1) / C::kKeys);
   const int units = posmax < 0 ? 0 : usink + posmax / C::kKeys - ulow + 1;
 
-  float* cpart = reinterpret_cast<float*>(smem + C::kOffC);
+  float* gpart = reinterpret_cast<float*>(smem + C::kOffC);      // from the ranks
+  float* gmax = gpart + C::kCols * D + 4 * C::kMaxRanks;        // [rank][col]
+  float* gsum = gmax + C::kMaxRanks * C::kCols;
   float* wref = reinterpret_cast<float*>(smem + C::kOffStat);   // [warp][col]
   float* wmax = wref + C::kWarps * C::kCols;
   float* wsum = wmax + C::kWarps * C::kCols;
-  float* cmax = wsum + C::kWarps * C::kCols;                    // [col]
-  float* csum = cmax + C::kCols;
-  float* qscale = csum + C::kCols;
+  float* qscale = wsum + C::kWarps * C::kCols;                  // [col]
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar) + warp * C::kStages;
   uint8_t* ring = smem + (size_t)warp * C::kStages * C::kStage;
 
@@ -241,6 +264,20 @@ __global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
   }
   __syncwarp();
 
+  // the queries' loads go out first: they are used after the stages have been asked for
+  float xq[NT][D / 32];  // columns warp, warp + 8, ...; dims lane, lane + 32, ...
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int col = n * 8 + warp, cc = c0 + col, row = cc / G, h = hkv * G + cc % G;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) {
+      xq[n][e] = 0.f;
+      if (col < ncol) {
+        const size_t o = (size_t)(sq.r0 + row) * p.q_stride + (size_t)h * D + lane + 32 * e;
+        xq[n][e] = F32 ? static_cast<const float*>(p.q)[o] : bf16_to_f32(static_cast<const uint16_t*>(p.q)[o]);
+      }
+    }
+  }
   // ---- this warp's stages: gw, gw + nw, ...
   const int gw = rank * C::kWarps + warp, nw = csize * C::kWarps;
   const int mine = gw < units ? (units - gw + nw - 1) / nw : 0;
@@ -284,17 +321,10 @@ __global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
 
   // ---- queries: the parts of every column in the order the products read them.  A column's queries are
   // scaled by a power of two so that the largest is in [2^14, 2^15) (FMT 1: f16 holds them).
-  for (int col = warp; col < C::kCols; col += C::kWarps) {
-    const int cc = c0 + col, row = cc / G, h = hkv * G + cc % G;
-    float x[D / 32];  // dims lane, lane + 32, ...
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) {
-      x[e] = 0.f;
-      if (col < ncol) {
-        const size_t o = (size_t)(sq.r0 + row) * p.q_stride + (size_t)h * D + lane + 32 * e;
-        x[e] = F32 ? static_cast<const float*>(p.q)[o] : bf16_to_f32(static_cast<const uint16_t*>(p.q)[o]);
-      }
-    }
+  for (int n = 0; n < NT; ++n) {
+    const int col = n * 8 + warp;
+    const float(&x)[D / 32] = xq[n];
     float up = 1.f;
     if constexpr (FMT == 1) {
       float am = 0.f;
@@ -689,14 +719,15 @@ __global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int col = n * 8 + 2 * lt + e;
-      float* wp = wpart + ((size_t)warp * C::kCols + col) * C::kLd;
+      float* wp = wpart + (size_t)warp * C::kPartFloats;
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         if constexpr (FMT == 1) {
-          *reinterpret_cast<float2*>(wp + lg * (D / 8) + 2 * i) = make_float2(o[n][i][e], o[n][i][2 + e]);
+          reinterpret_cast<float2*>(wp)[(n * MT + i) * C::kPair + (2 * lt + e) * 10 + lg] =
+              make_float2(o[n][i][e], o[n][i][2 + e]);
         } else {
-          wp[16 * i + lg] = o[n][i][e];
-          wp[16 * i + 8 + lg] = o[n][i][2 + e];
+          wp[col * C::kLd + 16 * i + lg] = o[n][i][e];
+          wp[col * C::kLd + 16 * i + 8 + lg] = o[n][i][2 + e];
         }
       }
       if (lg == 0) {
@@ -706,100 +737,81 @@ __global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
       }
     }
   __syncthreads();
-  if (threadIdx.x < C::kCols) {
-    const int col = threadIdx.x;
+  auto peer = [&](const void* a, int r) {
+    uint32_t ra;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(smem_u32(a)), "r"(r));
+    return ra;
+  };
+  if (csize > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  // The CTA's maximum and sum of every column, to every rank.
+  for (int e = threadIdx.x; e < csize * C::kCols; e += 256) {
+    const int col = e % C::kCols, r = e / C::kCols;
     float M = -INFINITY, L = 0.f;
 #pragma unroll
     for (int w = 0; w < C::kWarps; ++w) M = fmaxf(M, wmax[w * C::kCols + col]);
 #pragma unroll
     for (int w = 0; w < C::kWarps; ++w) {
-      const float mw = wmax[w * C::kCols + col], rw = wref[w * C::kCols + col], lw = wsum[w * C::kCols + col];
-      L += mw == -INFINITY ? lw : lw * ex2f(mw - M);             // lw: 0, or NaN
-      wref[w * C::kCols + col] = rw == -INFINITY ? 0.f : ex2f(rw - M);  // the factor of the warp's outputs
+      const float mw = wmax[w * C::kCols + col], lw = wsum[w * C::kCols + col];
+      L += mw == -INFINITY ? lw : lw * ex2f(mw - M);  // lw: 0, or NaN
     }
-    cmax[col] = M;
-    csum[col] = L;
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer(gmax + rank * C::kCols + col, r)), "f"(M) : "memory");
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer(gsum + rank * C::kCols + col, r)), "f"(L) : "memory");
   }
-  __syncthreads();
-  const int quads = ncol * (D / 4);  // 4 dims of a column each
+  // The CTA's outputs, 4 dims of a column each, to the rank that finishes them.
+  const int quads = ncol * (D / 4), share = (quads + csize - 1) / csize;
   for (int e = threadIdx.x; e < quads; e += 256) {
     const int col = e / (D / 4), d = e % (D / 4) * 4;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < C::kWarps; ++w) M = fmaxf(M, wmax[w * C::kCols + col]);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < C::kWarps; ++w) {
-      const float f = wref[w * C::kCols + col];
-      if (f != 0.f) {
-        const float4 v = *reinterpret_cast<const float4*>(wpart + ((size_t)w * C::kCols + col) * C::kLd + d);
+      const float rw = wref[w * C::kCols + col];
+      const float f = rw == -INFINITY ? 0.f : ex2f(rw - M);
+      const float* wp = wpart + (size_t)w * C::kPartFloats;
+      float4 v;
+      if constexpr (FMT == 1) {
+        const float2* w2 = reinterpret_cast<const float2*>(wp) +
+                           ((col / 8) * MT + d % (D / 8) / 2) * C::kPair + (col % 8) * 10 + d / (D / 8);
+        const float2 v0 = w2[0], v1 = w2[C::kPair];
+        v = make_float4(v0.x, v0.y, v1.x, v1.y);
+      } else {
+        v = *reinterpret_cast<const float4*>(wp + col * C::kLd + d);
+      }
+      if (f != 0.f) {  // else what is there may be anything
         s.x = fmaf(v.x, f, s.x);
         s.y = fmaf(v.y, f, s.y);
         s.z = fmaf(v.z, f, s.z);
         s.w = fmaf(v.w, f, s.w);
       }
     }
-    *reinterpret_cast<float4*>(cpart + (size_t)e * 4) = s;
+    const int r = e / share;
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                     peer(gpart + (size_t)(rank * share + e - r * share) * 4, r)),
+                 "f"(s.x), "f"(s.y), "f"(s.z), "f"(s.w)
+                 : "memory");
   }
-  // ---- the CTAs of the cluster: each finishes its share of the outputs, adding the ranks in order
-  auto cluster_sync = [&]() {
+  if (csize > 1)
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-  };
-  auto peer = [&](const void* a, int r) {
-    uint32_t ra;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(smem_u32(a)), "r"(r));
-    return ra;
-  };
-  float* fac = wmax;    // [rank][col]: factor of a rank's outputs (16 ranks: over wmax and wsum)
-  float* total = qscale;
-  if (csize > 1) {
-    cluster_sync();
-    for (int e = threadIdx.x; e < csize * C::kCols; e += 256) {
-      float v;
-      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer(cmax + e % C::kCols, e / C::kCols)) : "memory");
-      fac[e] = v;
-    }
+  else
     __syncthreads();
-    if (threadIdx.x < C::kCols) {
-      const int col = threadIdx.x;
-      float M = -INFINITY, L = 0.f;
-      for (int r = 0; r < csize; ++r) M = fmaxf(M, fac[r * C::kCols + col]);
-      for (int r = 0; r < csize; ++r) {
-        float lr;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(lr) : "r"(peer(csum + col, r)) : "memory");
-        const float mr = fac[r * C::kCols + col];
-        const float f = mr == -INFINITY ? 0.f : ex2f(mr - M);
-        fac[r * C::kCols + col] = f;
-        L += mr == -INFINITY ? lr : lr * f;  // lr: 0, or NaN
-      }
-      total[col] = L;
-    }
-    __syncthreads();
-  } else {
-    if (threadIdx.x < C::kCols) total[threadIdx.x] = csum[threadIdx.x];
-    __syncthreads();
-  }
-  const int share = (quads + csize - 1) / csize;
+  // ---- this rank's share of the outputs, the ranks added in order
   for (int e = rank * share + threadIdx.x; e < min(quads, (rank + 1) * share); e += 256) {
     const int col = e / (D / 4), d = e % (D / 4) * 4;
-    float y[4] = {0.f, 0.f, 0.f, 0.f};
-    if (csize > 1) {
-#pragma unroll 4
-      for (int r = 0; r < csize; ++r) {
-        const float f = fac[r * C::kCols + col];
-        float4 v;
-        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                     : "r"(peer(cpart + (size_t)e * 4, r))
-                     : "memory");
-        if (f != 0.f) {
-          y[0] = fmaf(v.x, f, y[0]);
-          y[1] = fmaf(v.y, f, y[1]);
-          y[2] = fmaf(v.z, f, y[2]);
-          y[3] = fmaf(v.w, f, y[3]);
-        }
-      }
-    } else {
-      *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(cpart + (size_t)e * 4);
+    float M = -INFINITY, L = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int r = 0; r < csize; ++r) M = fmaxf(M, gmax[r * C::kCols + col]);
+    for (int r = 0; r < csize; ++r) {
+      const float mr = gmax[r * C::kCols + col], lr = gsum[r * C::kCols + col];
+      const float4 v = *reinterpret_cast<const float4*>(gpart + (size_t)(r * share + e - rank * share) * 4);
+      const float f = mr == -INFINITY ? 0.f : ex2f(mr - M);
+      L += mr == -INFINITY ? lr : lr * f;  // lr: 0, or NaN
+      y[0] = fmaf(v.x, f, y[0]);
+      y[1] = fmaf(v.y, f, y[1]);
+      y[2] = fmaf(v.z, f, y[2]);
+      y[3] = fmaf(v.w, f, y[3]);
     }
-    const float L = total[col], inv = L == 0.f ? 0.f : 1.f / L;
+    const float inv = 1.f / L;
     const int cc = c0 + col;
     const size_t oo = (size_t)(sq.r0 + cc / G) * p.out_stride + (size_t)(hkv * G + cc % G) * D + d;
 #pragma unroll
@@ -821,7 +833,6 @@ __global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
         for (int i = 0; i < 4; ++i) o4[i] = w[i];
     }
   }
-  if (csize > 1) cluster_sync();  // nobody leaves while a peer may read its shared memory
 }
 
 template <int D, int FMT, int NT, int F32>
@@ -838,12 +849,19 @@ cudaError_t launch_decode_t(const CUtensorMap& mk, const CUtensorMap& mv, const 
   if (e) return e;
   const int G = p.Hq / p.c.Hkv;
   const int64_t tiles = ((int64_t)p.c.max_rows * G + C::kCols - 1) / C::kCols;
-  // CTAs per group: enough to give every SM two, as long as a warp still gets a stage.
+  // CTAs per group: enough to fill the SMs (4-bit: two CTAs each), as long as a warp still gets a stage
+  // (measured: one more doubling costs 5-30%, one less leaves SMs idle).  16, beyond the portable
+  // cluster size, starts slowly and pays only for one long sequence (131072 positions, 8 KV heads: 101 ->
+  // 79 us; 4096 positions: 8.9 -> 11 us).
   const int64_t keys = p.window > 0 ? std::min<int64_t>(p.c.max_len, (int64_t)p.window + p.sinks + 8) : p.c.max_len;
   const int64_t groups = tiles * p.c.Hkv * p.c.n_seq;
+  const int64_t units = (keys + C::kKeys - 1) / C::kKeys;
+  const int slots = (FMT ? 2 : 1) * 152;
   int cs = 1;
-  while (cs < 16 && groups * cs < 2 * 152 && (int64_t)cs * C::kWarps * C::kKeys < keys) cs *= 2;
+  while (cs < 8 && groups * cs < slots && (int64_t)cs * C::kWarps < units) cs *= 2;
+  if (cs == 8 && groups * 8 < 152 && units >= 1024) cs = 16;
   if (tiles * cs > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  const int sorted = p.c.n_seq > 1 && p.c.n_seq <= kSortMax && groups * cs > 152 ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * cs), p.c.Hkv, p.c.n_seq);
   cfg.blockDim = dim3(256);
@@ -856,16 +874,21 @@ cudaError_t launch_decode_t(const CUtensorMap& mk, const CUtensorMap& mv, const 
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_cache_decode<D, FMT, NT, F32>, mk, mv, p, cs);
+  return cudaLaunchKernelEx(&cfg, k_cache_decode<D, FMT, NT, F32>, mk, mv, p, cs, sorted);
 }
 
 template <int D, int FMT, int F32>
 cudaError_t launch_decode_n(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnParams& p,
                             cudaStream_t s) {
+  // Columns of a tile.  bf16 pages: as many as fit the registers share a read (16 sequences x 5 rows x 4
+  // heads: 27 us with 24 columns, 32 with 8).  4-bit pages: 8; more would leave one CTA an SM, and the
+  // products' latency shows (22 us with 8, 28 with 24).
   const int64_t cols = (int64_t)p.c.max_rows * (p.Hq / p.c.Hkv);
-  if (cols <= 8) return launch_decode_t<D, FMT, 1, F32>(mk, mv, p, s);
-  if (cols <= 16) return launch_decode_t<D, FMT, 2, F32>(mk, mv, p, s);
-  return launch_decode_t<D, FMT, 3, F32>(mk, mv, p, s);
+  if constexpr (FMT == 0) {
+    if (cols > 16) return launch_decode_t<D, FMT, 3, F32>(mk, mv, p, s);
+    if (cols > 8) return launch_decode_t<D, FMT, 2, F32>(mk, mv, p, s);
+  }
+  return launch_decode_t<D, FMT, 1, F32>(mk, mv, p, s);
 }
 
 }  // namespace

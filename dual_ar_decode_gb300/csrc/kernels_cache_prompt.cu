@@ -1,0 +1,700 @@
+// Attention of many rows per sequence over a paged KV cache on the tensor
+// cores (sm_103a): the prompt form of tf_op_attention_cache for bfloat16 rows,
+// over bf16 and 4-bit pages.
+//
+// out = sum_j p_j v_j, p = softmax_j(scale q.k_j) over what a row sees.  With
+// hundreds of rows per K / V read the two products are the bound, so they run as
+// tcgen05.mma (M = 128, bf16, fp32 in TMEM):
+//   * A CTA takes 256 (row, query head) pairs of one KV head, so that the heads
+//     of a group and 256 / G rows share every K and V tile, as two tiles A and B
+//     of 128 (a pair is a TMEM lane).  While a warpgroup turns the scores of A
+//     into probabilities the tensor core multiplies B's, and the other way round.
+//   * TMEM (512 columns): scores of A and B (128 columns each), outputs of A and
+//     B.  The probabilities go back into the first 64 columns of their scores
+//     as bf16 and are the second product's A operand straight from there: no
+//     shared-memory trip, and shared memory holds Q, 2 K and 2 V tiles.
+//   * A key tile is four pages of the list (sink pages, then the window's), each
+//     with its own base position, so that neither the sinks nor a window that
+//     starts inside a tile costs a tile of its own.
+//   * bf16 pages come by TMA (128-byte swizzle).  4-bit pages are converted by
+//     four warps: e2m1 x e4m3 has at most 6 significant bits and is exact in bf16;
+//     K's row scale multiplies the scores and V's the probabilities, in float32.
+//   * The maximum is replaced, and O rescaled in TMEM, only when a score exceeds
+//     it by more than 2^8.  Probabilities enter as bf16 (half a step: 2^-8 of
+//     each, as much as the output's own rounding); their sum is of the unrounded
+//     ones, in float32.
+//   * Tiles that some row does not see whole are masked, and V rows that no row
+//     sees are zeroed in shared memory (0 x NaN is NaN); a V row with an infinity
+//     or a NaN that only some rows see is zeroed too and made a NaN probability
+//     of the rows that see it.
+// Every wait is bounded; the TMEM columns are always released.
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "cache.cuh"
+#include "common.cuh"
+#include "device_once.h"
+#include "kernels.h"
+#include "tensor_map.h"
+
+namespace tf {
+
+namespace {
+
+constexpr float kGrow = 8.0f;    // log2 of the growth at which the maximum is replaced
+constexpr int kInfo = 4;         // tiles of which the position / scale records are kept
+constexpr int kNowhere = 0x3FFFFFFF;  // base position of a quarter that holds nothing
+
+template <int D, int FMT>
+struct PromptCfg {
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kTile = 128 * D * 2;              // 128 rows of Q, K or V
+  static constexpr int kSlots = 2;                       // K tiles, and V tiles, in flight
+  static constexpr size_t kOffK = 2 * (size_t)kTile;
+  static constexpr size_t kOffV = kOffK + (size_t)kSlots * kTile;
+  static constexpr size_t kOffInfo = kOffV + (size_t)kSlots * kTile;
+  // per kept tile: 4 base positions, 4 poison words, and for 4-bit pages 128 K and V row scales
+  static constexpr int kInfoBytes = 32 + (FMT ? 2 * 128 * 4 : 0);
+  static constexpr size_t kOffBar = kOffInfo + (size_t)kInfo * kInfoBytes;
+  static constexpr size_t kSmem = 1024 + kOffBar + 24 * 8 + 16;
+  static constexpr int kThreads = FMT ? 32 * 13 : 32 * 10;  // 8 softmax, 1 MMA, 1 TMA or 4 converting warps
+  static constexpr uint32_t kCols = 512;
+  // kind::f16, fp32 accumulate, bf16 operands, M = 128.  S: B = K tile, K-major, N = 128.
+  // O: B = V tile, MN-major (bit 16), N = D.
+  static constexpr uint32_t kIdescS =
+      (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+  static constexpr uint32_t kIdescO = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) |
+                                      ((uint32_t)(D >> 3) << 17) | ((128u >> 4) << 24);
+};
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer_ns() - t0 > kWaitBudgetNs) return false;
+  return true;
+}
+// the same, one answer for the warp (what follows is warp-collective)
+__device__ __forceinline__ bool bar_wait_warp(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity) ? 1 : 0) != 0;
+}
+
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// K-major operand tile: 8-row groups of 128-byte rows, 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | static_cast<uint64_t>(1) << 16 |
+         static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
+}
+// MN-major operand tile: 64-element column blocks 16 KB apart.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | static_cast<uint64_t>(16384 >> 4) << 16 |
+         static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+
+__device__ __forceinline__ void tm_ld32(uint32_t addr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tm_st32(uint32_t addr, const float (&v)[32]) {
+  uint32_t r[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ void e2m1x8(uint32_t v, uint32_t (&h)[4]) {
+  asm("{.reg .b8 b0, b1, b2, b3; mov.b32 {b0, b1, b2, b3}, %4;"
+      " cvt.rn.f16x2.e2m1x2 %0, b0; cvt.rn.f16x2.e2m1x2 %1, b1;"
+      " cvt.rn.f16x2.e2m1x2 %2, b2; cvt.rn.f16x2.e2m1x2 %3, b3;}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(v));
+}
+__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t v) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(v)));
+  return h;
+}
+__device__ __forceinline__ float2 scaled(uint32_t v, uint32_t s) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(s));
+  return __half22float2(*reinterpret_cast<const __half2*>(&d));
+}
+// 16-byte chunk of row r, chunk ch of the row, in the swizzled tile layout.
+__device__ __forceinline__ uint4* chunk_at(uint8_t* tile, int r, int ch) {
+  return reinterpret_cast<uint4*>(tile + (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+}
+
+// Bits of the 32 positions from base that a row at `pos` sees.
+__device__ __forceinline__ uint32_t ones(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
+__device__ __forceinline__ uint32_t sees(int base, int pos, int low, int sinks) {
+  return ones(pos - base + 1) & (~ones(low - base) | ones(sinks - base));
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
+    k_cache_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                   const CacheAttnParams p) {
+  using C = PromptCfg<D, FMT>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sk = smem + C::kOffK;
+  uint8_t* sv = smem + C::kOffV;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t *k_full = bar, *k_empty = bar + 2, *v_full = bar + 4, *v_empty = bar + 6;  // [2] each
+  uint64_t *s_full = bar + 8, *p_full = bar + 10, *o_done = bar + 12, *drained = bar + 14, *cleaned = bar + 15;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 16);
+  volatile uint32_t* failed = tmem_slot + 1;
+
+  const CacheBatch& c = p.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hkv = blockIdx.y, b = blockIdx.z;
+  const int G = p.Hq / c.Hkv;
+  const SeqRows sq = cache_seq(c, b);
+  const int tile = static_cast<int>(gridDim.x - 1 - blockIdx.x);  // the last rows, which see most, first
+  const int c0 = tile * 256, ncol = min(256, sq.n * G - c0);
+  if (ncol <= 0) return;
+  const int first = sq.len - sq.n;
+  const int posmin = first + c0 / G, posmax = first + (c0 + ncol - 1) / G;
+  const bool win = p.window > 0;
+  const int lowmin = win ? max(0, posmin - p.window + 1) : 0;
+  const int lowmax = win ? max(0, posmax - p.window + 1) : 0;
+  const int sinks = win ? p.sinks : 0;
+  // The list of pages: the sinks' that the windows do not reach, then lowmin .. posmax.
+  const int plow = lowmin / kKvPage;
+  const int psink = min(plow, (min(sinks, lowmin) + kKvPage - 1) / kKvPage);
+  const int pages = posmax < 0 ? 0 : psink + posmax / kKvPage - plow + 1;
+  const int nt = (pages + 3) / 4;
+  auto base_at = [&](int u) { return (u < psink ? u : plow + u - psink) * kKvPage; };
+  struct Info {
+    int base[4];
+    uint32_t poison[4];
+    float ks[FMT ? 128 : 1], vs[FMT ? 128 : 1];
+  };
+  auto info = [&](int j) { return reinterpret_cast<Info*>(smem + C::kOffInfo + (j % kInfo) * C::kInfoBytes); };
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_full[i], FMT ? 128 : 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], FMT ? 128 : 1);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&o_done[i], 1);
+    }
+    mbar_init(drained, 1);
+    mbar_init(cleaned, 256);
+    *failed = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(C::kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // Q: pair m of the CTA is row (c0 + m) / G, head (c0 + m) % G; rows past the last pair are zero.
+  for (int e = threadIdx.x; e < 256 * (D / 8); e += C::kThreads) {
+    const int m = e / (D / 8), ch = e % (D / 8), cc = c0 + m;
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (m < ncol) {
+      const uint16_t* src = static_cast<const uint16_t*>(p.q) + (size_t)(sq.r0 + cc / G) * p.q_stride +
+                            (size_t)(hkv * G + cc % G) * D + ch * 8;
+      if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+        x = *reinterpret_cast<const uint4*>(src);
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = src[2 * i] | static_cast<uint32_t>(src[2 * i + 1]) << 16;
+        x = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    *chunk_at(smem + (m >> 7) * C::kTile, m & 127, ch) = x;
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 8) {
+    // ---------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      bool ok = true;
+      auto score = [&](int x, int j) {  // S_x = Q_x K(j)^T
+        const uint32_t qb = smem_u32(smem) + x * C::kTile, kb = smem_u32(sk) + (j & 1) * C::kTile;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+          mma_ss(tmem + x * 128, desc_k(qb + off), desc_k(kb + off), C::kIdescS, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(&s_full[x]);
+      };
+      if (nt > 0) {
+        ok = bar_wait(&k_full[0], 0);
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        if (ok) {
+          score(0, 0);
+          score(1, 0);
+          mma_commit(&k_empty[0]);
+        }
+      }
+      for (int j = 0; ok && j < nt; ++j) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          ok = ok && bar_wait(&p_full[x], j & 1) && (x || bar_wait(&v_full[j & 1], (j >> 1) & 1));
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint32_t vb = smem_u32(sv) + (j & 1) * C::kTile;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, desc_mn(vb + kk * 2048), C::kIdescO,
+                   (j > 0 || kk > 0) ? 1u : 0u);
+          if (x) mma_commit(&v_empty[j & 1]);
+          if (j + 1 < nt) {
+            if (!x) {
+              ok = bar_wait(&k_full[(j + 1) & 1], ((j + 1) >> 1) & 1);
+              if (!ok) break;
+              asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            }
+            score(x, j + 1);  // after the product that reads P_x, in issue order; its commit covers both
+            if (x) mma_commit(&k_empty[(j + 1) & 1]);
+          } else {
+            mma_commit(&o_done[x]);
+          }
+        }
+      }
+      if (!ok) *failed = 1;
+      mma_commit(drained);  // nothing may be in flight when the columns are released
+      if (!bar_wait(drained, 0)) *failed = 1;
+    }
+  } else if (warp > 8) {
+    if constexpr (FMT == 0) {
+      // -------------------------------------------------------------- TMA producer
+      if (lane == 0) {
+        int done = 0;
+        for (; done < nt; ++done) {
+          const int j = done, s = j & 1;
+          int pg[4];
+          uint32_t boxes = 0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int u = 4 * j + q;
+            pg[q] = u < pages ? cache_page(c, b, base_at(u) / kKvPage) : -1;
+            boxes += pg[q] >= 0 ? 1u : 0u;
+          }
+          if (j >= 2 && !bar_wait(&k_empty[s], ((j >> 1) - 1) & 1)) break;
+          Info* in = info(j);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            in->base[q] = pg[q] >= 0 ? base_at(4 * j + q) : kNowhere;
+            in->poison[q] = 0;
+          }
+          auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* full) {
+            mbar_arrive_expect_tx(full, boxes * (kKvPage * D * 2));
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (pg[q] >= 0)
+                for (int x = 0; x < C::kBoxes; ++x)
+                  tma_box(smem_u32(dst) + x * 16384 + q * (kKvPage * 128), map, x * 64,
+                          (pg[q] * c.Hkv + hkv) * kKvPage, full);
+          };
+          load(&map_k, sk + s * C::kTile, &k_full[s]);
+          if (j >= 2 && !bar_wait(&v_empty[s], ((j >> 1) - 1) & 1)) {
+            bar_wait(&k_full[s], (j >> 1) & 1);
+            break;
+          }
+          load(&map_v, sv + s * C::kTile, &v_full[s]);
+        }
+        if (done < nt) *failed = 1;
+        // every copy has landed before the CTA leaves
+        for (int j = max(0, done - 2); j < done; ++j)
+          if (!bar_wait(&k_full[j & 1], (j >> 1) & 1) || !bar_wait(&v_full[j & 1], (j >> 1) & 1)) break;
+      }
+    } else {
+      // -------------------------------------------------------------- converting warps, one page of a tile each
+      using L = Kv4<D>;
+      constexpr int NI = D / 32;     // 16-byte pieces of K (and of V) a lane takes
+      constexpr int PR = D / 32;     // pieces of a K row
+      const int w = warp - 9;
+      uint4 kr[NI], vr[NI];
+      uint32_t ksb[NI], vsb[NI];
+      float krow, vrow;
+      int base;
+      // V piece i of this lane: unit of (position pair column j, block, t); the order differs by t so that the
+      // lanes' rows fall into different banks
+      auto v_unit = [&](int i) {
+        if constexpr (D == 128) return ((i + lane) & 3) * 32 + lane;
+        return i * 32 + lane;
+      };
+      auto fetch = [&](int j) {
+        const int u = 4 * j + w;
+        const int pg = u < pages ? cache_page(c, b, base_at(u) / kKvPage) : -1;
+        base = pg >= 0 ? base_at(u) : kNowhere;
+        krow = vrow = 0.f;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          kr[i] = vr[i] = make_uint4(0u, 0u, 0u, 0u);
+          ksb[i] = vsb[i] = 0;
+        }
+        if (pg < 0) return;
+        const size_t off = ((size_t)pg * c.Hkv + hkv) * L::kBytes;
+        const uint8_t *kp = c.K + off, *vp = c.V + off;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int e = i * 32 + lane;  // piece: row e / PR, elements 32 (e % PR) ..
+          kr[i] = __ldg(reinterpret_cast<const uint4*>(kp + e * 16));
+          ksb[i] = __ldg(reinterpret_cast<const uint16_t*>(kp + L::kCodes + e * 2));
+          const int v = v_unit(i);
+          vr[i] = __ldg(reinterpret_cast<const uint4*>(vp + v * 16));
+          vsb[i] = __ldg(reinterpret_cast<const uint16_t*>(vp + L::kCodes + (v % (D / 4)) / 4 * kKvPage +
+                                                           8 * (v & 3) + 2 * (v / (D / 4))));
+        }
+        krow = __ldg(reinterpret_cast<const float*>(kp + L::kRows) + lane);
+        vrow = __ldg(reinterpret_cast<const float*>(vp + L::kRows) + lane);
+      };
+      bool ok = true;
+      if (nt > 0) fetch(0);
+      for (int j = 0; j < nt; ++j) {
+        const int s = j & 1;
+        const bool whole = base + kKvPage - 1 <= posmin && (base >= lowmax || base + kKvPage <= sinks);
+        uint32_t dead = 0, poison = 0;
+        if (!whole) {
+          const int pos = base + lane;
+          dead = __ballot_sync(0xFFFFFFFFu, !(pos <= posmax && (pos >= lowmin || pos < sinks)));
+          uint32_t bad = 0;
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            const int v = v_unit(i), r = 8 * (v & 3) + 2 * (v / (D / 4));
+            bad |= (((vsb[i] & 0x7Fu) == 0x7Fu ? 1u : 0u) | ((vsb[i] & 0x7F00u) == 0x7F00u ? 2u : 0u)) << r;
+          }
+          poison = __reduce_or_sync(0xFFFFFFFFu, bad) & ~dead;
+        }
+        Info* in = info(j);
+        if (j >= 2 && !(ok = bar_wait_warp(&k_empty[s], ((j >> 1) - 1) & 1))) break;
+        if (lane == 0) {
+          in->base[w] = base;
+          in->poison[w] = poison;
+        }
+        in->ks[w * 32 + lane] = krow * p.scale_log2;
+        in->vs[w * 32 + lane] = (dead >> lane) & 1u ? 0.f : vrow;
+        uint8_t* kt = sk + s * C::kTile;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int e = i * 32 + lane, r = w * 32 + e / PR, q = e % PR;
+          const uint32_t words[4] = {kr[i].x, kr[i].y, kr[i].z, kr[i].w};
+          const uint32_t s2 = e4m3x2_f16(ksb[i]);
+          uint32_t o[16];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t h[4];
+            e2m1x8(words[x], h);
+            const uint32_t sd = __byte_perm(s2, 0, x < 2 ? 0x1010 : 0x3232);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const float2 f = scaled(h[y], sd);
+              o[4 * x + y] = pack_bf16(f.x, f.y);
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            *chunk_at(kt, r, 4 * q + x) = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        mbar_arrive(&k_full[s]);
+        if (j >= 2 && !(ok = bar_wait_warp(&v_empty[s], ((j >> 1) - 1) & 1))) break;
+        uint8_t* vt = sv + s * C::kTile;
+        dead |= poison;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int v = v_unit(i), r = 8 * (v & 3) + 2 * (v / (D / 4)), blk = (v % (D / 4)) / 4;
+          const uint32_t words[4] = {vr[i].x, vr[i].y, vr[i].z, vr[i].w};
+          uint32_t sb = vsb[i];
+          if ((dead >> r) & 1u) sb &= 0xFF00u;
+          if ((dead >> r) & 2u) sb &= 0x00FFu;
+          const uint32_t s2 = e4m3x2_f16(sb);
+          uint32_t o0[8], o1[8];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t h[4];
+            e2m1x8(words[x], h);
+#pragma unroll
+            for (int y = 0; y < 4; y += 2) {
+              const float2 f = scaled(h[y], s2), g = scaled(h[y + 1], s2);
+              o0[2 * x + y / 2] = pack_bf16(f.x, g.x);
+              o1[2 * x + y / 2] = pack_bf16(f.y, g.y);
+            }
+          }
+          const int row = w * 32 + r;
+          *chunk_at(vt, row, 2 * blk) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+          *chunk_at(vt, row, 2 * blk + 1) = make_uint4(o0[4], o0[5], o0[6], o0[7]);
+          *chunk_at(vt, row + 1, 2 * blk) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+          *chunk_at(vt, row + 1, 2 * blk + 1) = make_uint4(o1[4], o1[5], o1[6], o1[7]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        mbar_arrive(&v_full[s]);
+        if (j + 1 < nt) fetch(j + 1);
+      }
+      if (!ok && lane == 0) *failed = 1;
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax: one pair a thread
+    const int x = warp >> 2, m = threadIdx.x & 127;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + x * 128 + lanes, t_o = tmem + 256 + x * 128 + lanes;
+    const int col = x * 128 + m, cc = c0 + col;
+    const bool valid = col < ncol;
+    const int pos = valid ? first + cc / G : posmin;
+    const int low = win ? max(0, pos - p.window + 1) : 0;
+    float ref = -INFINITY, l = 0.f;
+    bool ok = true;
+    int cleanings = 0;
+    for (int j = 0; j < nt; ++j) {
+      if (!(ok = bar_wait_warp(&s_full[x], j & 1))) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const Info* in = info(j);
+      uint32_t see[4];
+      bool mine = true, tile_whole = true;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int bq = in->base[q];
+        see[q] = sees(bq, pos, low, sinks);
+        mine = mine && see[q] == 0xFFFFFFFFu;
+        tile_whole = tile_whole && bq + kKvPage - 1 <= posmin && (bq >= lowmax || bq + kKvPage <= sinks);
+      }
+      const bool whole = __all_sync(0xFFFFFFFFu, mine ? 1 : 0) != 0;
+      if (FMT == 0 && !tile_whole) {
+        // V rows that nobody sees, or that are not finite: zero (all 256 threads, half a row each)
+        ok = bar_wait_warp(&v_full[j & 1], (j >> 1) & 1);
+        const int r = threadIdx.x >> 1, q = r >> 5;
+        const int bq = in->base[q], kp = bq + (r & 31);
+        uint8_t* vt = sv + (j & 1) * C::kTile;
+        if (ok) {
+          const bool dead = bq == kNowhere || !(kp <= posmax && (kp >= lowmin || kp < sinks));
+          bool bad = false;
+          constexpr int H = D / 16;  // 16-byte chunks of half a row
+#pragma unroll
+          for (int ch = 0; ch < H; ++ch) {
+            const uint4 v = *chunk_at(vt, r, (threadIdx.x & 1) * H + ch);
+            const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              bad |= (w4[i] & 0x7F80u) == 0x7F80u || (w4[i] & 0x7F800000u) == 0x7F800000u;
+          }
+          bad = __shfl_xor_sync(0xFFFFFFFFu, bad ? 1 : 0, 1) || bad;
+          if (dead || bad)
+#pragma unroll
+            for (int ch = 0; ch < H; ++ch)
+              *chunk_at(vt, r, (threadIdx.x & 1) * H + ch) = make_uint4(0u, 0u, 0u, 0u);
+          if (bad && !dead && !(threadIdx.x & 1))
+            atomicOr(const_cast<uint32_t*>(&in->poison[q]), 1u << (r & 31));
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        // the tile's rows are all done when both warpgroups have come here (a wait that ends, unlike a CTA
+        // barrier, should one of them have given up)
+        mbar_arrive(cleaned);
+        ok = bar_wait_warp(cleaned, cleanings++ & 1) && ok;
+        if (!ok) break;
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float s[32];
+        tm_ld32(t_s + q * 32, s);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          if constexpr (FMT == 1) s[i] *= in->ks[q * 32 + i];
+          if (!whole) s[i] = (see[q] >> i) & 1u ? s[i] : -INFINITY;
+          mx = fmaxf(mx, s[i]);
+        }
+      }
+      if constexpr (FMT == 0) mx *= p.scale_log2;
+      const bool grow = mx > ref + kGrow;
+      const float alpha = grow ? (ref == -INFINITY ? 0.f : ex2f(ref - mx)) : 1.f;
+      if (grow) {
+        l *= alpha;
+        ref = mx;
+      }
+      if (j > 0 && __any_sync(0xFFFFFFFFu, grow)) {  // the product with the previous tile is done (s_full)
+#pragma unroll 1
+        for (int d = 0; d < D; d += 32) {
+          float t[32];
+          tm_ld32(t_o + d, t);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) t[i] *= alpha;
+          tm_st32(t_o + d, t);
+        }
+      }
+      const float nm = ref == -INFINITY ? 0.f : -ref;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float s[32];
+        tm_ld32(t_s + q * 32, s);
+        const uint32_t poison = whole ? 0u : in->poison[q];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float e = FMT ? ex2f(fmaf(s[i], in->ks[q * 32 + i], nm)) : ex2f(fmaf(s[i], p.scale_log2, nm));
+          if (!whole) {
+            const bool on = (see[q] >> i) & 1u;
+            if (on && ((poison >> i) & 1u)) e = __int_as_float(0x7FFFFFFF);
+            e = on ? e : 0.f;
+            sum[i & 3] += e;
+            if constexpr (FMT == 1) e = on ? e * in->vs[q * 32 + i] : 0.f;
+          } else {
+            sum[i & 3] += e;
+            if constexpr (FMT == 1) e *= in->vs[q * 32 + i];
+          }
+          s[i] = e;
+        }
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(s[2 * i], s[2 * i + 1]);
+        tm_st16(t_s + q * 16, pk);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      mbar_arrive(&p_full[x]);
+    }
+    if (ok && nt > 0) ok = bar_wait_warp(&o_done[x], 0);
+    if (ok) {
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const float inv = 1.f / l;
+      uint16_t* dst = static_cast<uint16_t*>(p.out) + (size_t)(sq.r0 + cc / G) * p.out_stride +
+                      (size_t)(hkv * G + cc % G) * D;
+#pragma unroll 1
+      for (int d = 0; d < D; d += 32) {
+        float t[32];
+        if (nt > 0) {
+          tm_ld32(t_o + d, t);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) t[i] = 0.f;
+        }
+        if (valid) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = l == 0.f ? 0u : pack_bf16(t[2 * i] * inv, t[2 * i + 1] * inv);
+          if ((reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<uint4*>(dst + d + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              dst[d + 2 * i] = static_cast<uint16_t>(w[i]);
+              dst[d + 2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
+            }
+          }
+        }
+        __syncwarp();
+      }
+    } else if (lane == 0) {
+      *failed = 1;
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0 && *failed) cache_flag(c, TF_CACHE_TIMEOUT);
+  if (warp == 8) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols) : "memory");
+  }
+}
+
+template <int D, int FMT>
+cudaError_t launch_prompt_t(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnParams& p,
+                            cudaStream_t s) {
+  using C = PromptCfg<D, FMT>;
+  static DeviceOnce once;
+  cudaError_t e = device_once(once, [] {
+    return cudaFuncSetAttribute(k_cache_prompt<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  });
+  if (e) return e;
+  const int64_t tiles = ((int64_t)p.c.max_rows * (p.Hq / p.c.Hkv) + 255) / 256;
+  if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  k_cache_prompt<D, FMT><<<dim3(static_cast<unsigned>(tiles), p.c.Hkv, p.c.n_seq), C::kThreads, C::kSmem, s>>>(mk, mv, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_prompt(const CacheAttnParams& p, cudaStream_t s) {
+  if (p.f32) return cudaErrorInvalidValue;
+  CUtensorMap mk = {}, mv = {};
+  if (p.c.fmt == 0) {
+    const uint64_t rows = (uint64_t)p.c.n_pages * p.c.Hkv * kKvPage;
+    if (!make_map(&mk, p.c.K, rows, p.c.D, kKvPage) || !make_map(&mv, p.c.V, rows, p.c.D, kKvPage))
+      return cudaErrorInvalidValue;
+    return p.c.D == 128 ? launch_prompt_t<128, 0>(mk, mv, p, s) : launch_prompt_t<64, 0>(mk, mv, p, s);
+  }
+  return p.c.D == 128 ? launch_prompt_t<128, 1>(mk, mv, p, s) : launch_prompt_t<64, 1>(mk, mv, p, s);
+}
+
+}  // namespace tf

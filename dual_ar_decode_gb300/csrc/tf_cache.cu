@@ -10,6 +10,8 @@ namespace {
 
 using namespace tf;
 
+constexpr int64_t kPromptPairs = 64;
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 bool batch_of(const tf_kv_cache* c, CacheBatch* b) {
@@ -94,7 +96,10 @@ tf_status tf_op_attention_cache(const tf_kv_cache* cache, const void* q, int64_t
   p.sinks = sinks < (1 << 30) ? sinks : 1 << 30;
   const double sc = scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)p.c.D);
   p.scale_log2 = static_cast<float>(sc * 1.4426950408889634);
-  return launch_cache_decode(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TF_OK : TF_E_CUDA;
+  // bfloat16 rows that fill a good part of a 256-pair tile go to the tensor-core kernel
+  const bool many = !p.f32 && (int64_t)p.c.max_rows * (n_heads / p.c.Hkv) >= kPromptPairs;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return (many ? launch_cache_prompt(p, s) : launch_cache_decode(p, s)) == cudaSuccess ? TF_OK : TF_E_CUDA;
 }
 
 tf_status tf_op_cache_append(const tf_kv_cache* cache, const void* k, const void* v, int64_t stride,
