@@ -32,6 +32,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "cache.cuh"
 #include "common.cuh"
@@ -182,6 +183,25 @@ __device__ __forceinline__ float2 scaled(uint32_t v, uint32_t s) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(s));
   return __half22float2(*reinterpret_cast<const __half2*>(&d));
+}
+// Two floats in one 64-bit operand of the packed float32 instructions.
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpair2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 // 16-byte chunk of row r, chunk ch of the row, in the swizzled tile layout.
 __device__ __forceinline__ uint4* chunk_at(uint8_t* tile, int r, int ch) {
@@ -561,63 +581,94 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
         ok = bar_wait_warp(cleaned, cleanings++ & 1) && ok;
         if (!ok) break;
       }
-      float mx = -INFINITY;
+      // One pass with the maximum of the tiles before: t = log2 of p, p packed in registers.  If some row's
+      // scores exceed it by more than 2^8 (always on its first tile), the scores are still in TMEM: the
+      // reference is replaced, O rescaled and the pass taken again.
+      uint32_t pk[4][16];
+      float sum, mx;
+      auto pass = [&](auto w_) {
+        constexpr bool kWhole = decltype(w_)::value;
+        const float nm = ref == -INFINITY ? 0.f : -ref;
+        const uint64_t nm2 = pair2(nm, nm), sc2 = pair2(p.scale_log2, p.scale_log2);
+        uint64_t sum2 = 0;  // two partial sums
+        mx = -INFINITY;
+        sum = 0.f;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float s[32];
-        tm_ld32(t_s + q * 32, s);
+        for (int q = 0; q < 4; ++q) {
+          float s[32];
+          tm_ld32(t_s + q * 32, s);
+          const uint32_t poison = kWhole ? 0u : in->poison[q];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          if constexpr (FMT == 1) s[i] *= in->ks[q * 32 + i];
-          if (!whole) s[i] = (see[q] >> i) & 1u ? s[i] : -INFINITY;
-          mx = fmaxf(mx, s[i]);
-        }
-      }
-      if constexpr (FMT == 0) mx *= p.scale_log2;
-      const bool grow = mx > ref + kGrow;
-      const float alpha = grow ? (ref == -INFINITY ? 0.f : ex2f(ref - mx)) : 1.f;
-      if (grow) {
-        l *= alpha;
-        ref = mx;
-      }
-      if (j > 0 && __any_sync(0xFFFFFFFFu, grow)) {  // the product with the previous tile is done (s_full)
-#pragma unroll 1
-        for (int d = 0; d < D; d += 32) {
-          float t[32];
-          tm_ld32(t_o + d, t);
+          for (int i = 0; i < 32; i += 4) {
+            float4 ks, vs;
+            if constexpr (FMT == 1) {
+              ks = *reinterpret_cast<const float4*>(in->ks + q * 32 + i);
+              vs = *reinterpret_cast<const float4*>(in->vs + q * 32 + i);
+            }
+            float t[4];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) t[i] *= alpha;
-          tm_st32(t_o + d, t);
-        }
-      }
-      const float nm = ref == -INFINITY ? 0.f : -ref;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int h = 0; h < 4; h += 2)
+              unpair2(fma2(pair2(s[i + h], s[i + h + 1]),
+                           FMT ? (h ? pair2(ks.z, ks.w) : pair2(ks.x, ks.y)) : sc2, nm2),
+                      t[h], t[h + 1]);
+            if constexpr (!kWhole) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float s[32];
-        tm_ld32(t_s + q * 32, s);
-        const uint32_t poison = whole ? 0u : in->poison[q];
+              for (int h = 0; h < 4; ++h) t[h] = (see[q] >> (i + h)) & 1u ? t[h] : -INFINITY;
+            }
+            mx = fmaxf(fmaxf(mx, fmaxf(t[0], t[1])), fmaxf(t[2], t[3]));
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float e = FMT ? ex2f(fmaf(s[i], in->ks[q * 32 + i], nm)) : ex2f(fmaf(s[i], p.scale_log2, nm));
-          if (!whole) {
-            const bool on = (see[q] >> i) & 1u;
-            if (on && ((poison >> i) & 1u)) e = __int_as_float(0x7FFFFFFF);
-            e = on ? e : 0.f;
-            sum[i & 3] += e;
-            if constexpr (FMT == 1) e = on ? e * in->vs[q * 32 + i] : 0.f;
-          } else {
-            sum[i & 3] += e;
-            if constexpr (FMT == 1) e *= in->vs[q * 32 + i];
+            for (int h = 0; h < 4; ++h) {
+              t[h] = ex2f(t[h]);
+              if constexpr (!kWhole) {
+                if ((poison & see[q]) >> (i + h) & 1u) t[h] = __int_as_float(0x7FFFFFFF);
+              }
+            }
+            sum2 = add2(sum2, add2(pair2(t[0], t[1]), pair2(t[2], t[3])));
+            if constexpr (FMT == 1) {
+              const float v4[4] = {vs.x, vs.y, vs.z, vs.w};
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                t[h] *= v4[h];
+                if constexpr (!kWhole) t[h] = (see[q] >> (i + h)) & 1u ? t[h] : 0.f;
+              }
+            }
+            pk[q][i / 2] = pack_bf16(t[0], t[1]);
+            pk[q][i / 2 + 1] = pack_bf16(t[2], t[3]);
           }
-          s[i] = e;
         }
-        uint32_t pk[16];
+        float a, b2;
+        unpair2(sum2, a, b2);
+        sum = a + b2;
+      };
+      auto run_pass = [&]() {
+        if (whole)
+          pass(std::integral_constant<bool, true>{});
+        else
+          pass(std::integral_constant<bool, false>{});
+      };
+      run_pass();
+      const bool grow = ref == -INFINITY ? mx > -INFINITY : mx > kGrow;
+      if (__any_sync(0xFFFFFFFFu, grow)) {
+        const float alpha = !grow || ref == -INFINITY ? 1.f : ex2f(-mx);
+        if (grow) {
+          l *= alpha;
+          ref = ref == -INFINITY ? mx : ref + mx;
+        }
+        if (j > 0) {  // the product with the previous tile is done (s_full)
+#pragma unroll 1
+          for (int d = 0; d < D; d += 32) {
+            float t[32];
+            tm_ld32(t_o + d, t);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(s[2 * i], s[2 * i + 1]);
-        tm_st16(t_s + q * 16, pk);
+            for (int i = 0; i < 32; ++i) t[i] *= alpha;
+            tm_st32(t_o + d, t);
+          }
+        }
+        run_pass();
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      l += sum;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tm_st16(t_s + q * 16, pk[q]);
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       mbar_arrive(&p_full[x]);
