@@ -56,11 +56,14 @@ struct PromptCfg {
   static constexpr size_t kOffK = 2 * (size_t)kTile;
   static constexpr size_t kOffV = kOffK + (size_t)kSlots * kTile;
   static constexpr size_t kOffInfo = kOffV + (size_t)kSlots * kTile;
-  // per kept tile: 4 base positions, 4 poison words, and for 4-bit pages 128 K and V row scales
-  static constexpr int kInfoBytes = 32 + (FMT ? 2 * 128 * 4 : 0);
+  // per kept tile: 4 base positions, poison words and whole flags, and for 4-bit pages 128 K and V row scales
+  static constexpr int kInfoBytes = 48 + (FMT ? 2 * 128 * 4 : 0);
   static constexpr size_t kOffBar = kOffInfo + (size_t)kInfo * kInfoBytes;
   static constexpr size_t kSmem = 1024 + kOffBar + 24 * 8 + 16;
-  static constexpr int kThreads = FMT ? 32 * 13 : 32 * 10;  // 8 softmax, 1 MMA, 1 TMA or 4 converting warps
+  // Warps: 8 softmax, then FMT 0: 1 MMA, 1 TMA, 2 that clean V; FMT 1: 4 converting, 1 MMA (and 3 idle ones, so
+  // that whole warpgroups can trade registers: the softmax takes what the others do not need).
+  static constexpr int kThreads = FMT ? 32 * 16 : 32 * 12;
+  static constexpr int kMmaWarp = FMT ? 12 : 8;
   static constexpr uint32_t kCols = 512;
   // kind::f16, fp32 accumulate, bf16 operands, M = 128.  S: B = K tile, K-major, N = 128.
   // O: B = V tile, MN-major (bit 16), N = D.
@@ -140,27 +143,33 @@ __device__ __forceinline__ void tm_ld32(uint32_t addr, float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void tm_st32(uint32_t addr, const float (&v)[32]) {
-  uint32_t r[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
+// The scores' and outputs' fragment: 16 lanes x 32 columns.  Register 4 i + 2 h + e of lane (g, t) is lane
+// g + 8 h of TMEM, column 8 i + 2 t + e (the shape of a warp-level product's accumulator), so a lane holds two
+// columns of several rows, and what belongs to a column is loaded once for all of them.
+__device__ __forceinline__ void tm_frag_ld(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
 }
-__device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tm_frag_st(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
       "%15, %16};" ::"r"(addr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// 16 lanes x 16 columns: register 2 i + h is lane g + 8 h, column 4 i + t.
+__device__ __forceinline__ void tm_pair_st(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t d;
@@ -203,6 +212,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 // 16-byte chunk of row r, chunk ch of the row, in the swizzled tile layout.
 __device__ __forceinline__ uint4* chunk_at(uint8_t* tile, int r, int ch) {
   return reinterpret_cast<uint4*>(tile + (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
@@ -226,7 +240,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
   uint8_t* sv = smem + C::kOffV;
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t *k_full = bar, *k_empty = bar + 2, *v_full = bar + 4, *v_empty = bar + 6;  // [2] each
-  uint64_t *s_full = bar + 8, *p_full = bar + 10, *o_done = bar + 12, *drained = bar + 14, *cleaned = bar + 15;
+  uint64_t *s_full = bar + 8, *p_full = bar + 10, *o_done = bar + 12, *drained = bar + 14, *v_clean = bar + 18;  // v_clean [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 16);
   volatile uint32_t* failed = tmem_slot + 1;
 
@@ -250,9 +264,13 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
   const int pages = posmax < 0 ? 0 : psink + posmax / kKvPage - plow + 1;
   const int nt = (pages + 3) / 4;
   auto base_at = [&](int u) { return (u < psink ? u : plow + u - psink) * kKvPage; };
+  auto quarter_whole = [&](int bq) {
+    return bq + kKvPage - 1 <= posmin && (bq >= lowmax || bq + kKvPage <= sinks) ? 1 : 0;
+  };
   struct Info {
-    int base[4];
-    uint32_t poison[4];
+    int base[4];          // position of the quarter's first key, kNowhere: nothing there
+    uint32_t poison[4];   // keys whose V row is not finite (mixed quarters)
+    int whole[4];         // every pair of the CTA sees every key of the quarter
     float ks[FMT ? 128 : 1], vs[FMT ? 128 : 1];
   };
   auto info = [&](int j) { return reinterpret_cast<Info*>(smem + C::kOffInfo + (j % kInfo) * C::kInfoBytes); };
@@ -262,17 +280,17 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
       mbar_init(&k_full[i], FMT ? 128 : 1);
       mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], FMT ? 128 : 1);
+      mbar_init(&v_clean[i], 64);
       mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 128);
       mbar_init(&o_done[i], 1);
     }
     mbar_init(drained, 1);
-    mbar_init(cleaned, 256);
     *failed = 0;
     fence_mbar_init();
   }
-  if (warp == 8) {
+  if (warp == C::kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"(C::kCols)
                  : "memory");
@@ -281,28 +299,32 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
   // Q: pair m of the CTA is row (c0 + m) / G, head (c0 + m) % G; rows past the last pair are zero.
   for (int e = threadIdx.x; e < 256 * (D / 8); e += C::kThreads) {
     const int m = e / (D / 8), ch = e % (D / 8), cc = c0 + m;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (m < ncol) {
-      const uint16_t* src = static_cast<const uint16_t*>(p.q) + (size_t)(sq.r0 + cc / G) * p.q_stride +
-                            (size_t)(hkv * G + cc % G) * D + ch * 8;
-      if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-        x = *reinterpret_cast<const uint4*>(src);
-      } else {
-        uint32_t w[4];
+    uint4* dst = chunk_at(smem + (m >> 7) * C::kTile, m & 127, ch);
+    const uint16_t* src = static_cast<const uint16_t*>(p.q) + (size_t)(sq.r0 + cc / G) * p.q_stride +
+                          (size_t)(hkv * G + cc % G) * D + ch * 8;
+    if (m >= ncol) {
+      *dst = make_uint4(0u, 0u, 0u, 0u);
+    } else if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+    } else {
+      uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = src[2 * i] | static_cast<uint32_t>(src[2 * i + 1]) << 16;
-        x = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+      for (int i = 0; i < 4; ++i) w[i] = src[2 * i] | static_cast<uint32_t>(src[2 * i + 1]) << 16;
+      *dst = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    *chunk_at(smem + (m >> 7) * C::kTile, m & 127, ch) = x;
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 8) {
+  // FMT 1: the softmax's warpgroups take registers from the other two: 256 x 168 + 256 x 88 = the launch's
+  // 512 x 128
+  if (warp >= 8) {
+  if constexpr (FMT == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (warp == C::kMmaWarp) {
     // ---------------------------------------------------------------- MMA issuer
     if (lane == 0) {
       bool ok = true;
@@ -327,7 +349,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
       for (int j = 0; ok && j < nt; ++j) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          ok = ok && bar_wait(&p_full[x], j & 1) && (x || bar_wait(&v_full[j & 1], (j >> 1) & 1));
+          ok = ok && bar_wait(&p_full[x], j & 1) && (x || bar_wait(FMT ? &v_full[j & 1] : &v_clean[j & 1], (j >> 1) & 1));
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           const uint32_t vb = smem_u32(sv) + (j & 1) * C::kTile;
@@ -353,10 +375,10 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
       mma_commit(drained);  // nothing may be in flight when the columns are released
       if (!bar_wait(drained, 0)) *failed = 1;
     }
-  } else if (warp > 8) {
+  } else {
     if constexpr (FMT == 0) {
       // -------------------------------------------------------------- TMA producer
-      if (lane == 0) {
+      if (warp == 9 && lane == 0) {
         int done = 0;
         for (; done < nt; ++done) {
           const int j = done, s = j & 1;
@@ -372,8 +394,10 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
           Info* in = info(j);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            in->base[q] = pg[q] >= 0 ? base_at(4 * j + q) : kNowhere;
+            const int bq = pg[q] >= 0 ? base_at(4 * j + q) : kNowhere;
+            in->base[q] = bq;
             in->poison[q] = 0;
+            in->whole[q] = quarter_whole(bq);
           }
           auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* full) {
             mbar_arrive_expect_tx(full, boxes * (kKvPage * D * 2));
@@ -395,64 +419,89 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
         // every copy has landed before the CTA leaves
         for (int j = max(0, done - 2); j < done; ++j)
           if (!bar_wait(&k_full[j & 1], (j >> 1) & 1) || !bar_wait(&v_full[j & 1], (j >> 1) & 1)) break;
+      } else if (warp >= 10) {
+        // ------------------------------------------------------------ V cleaners: in mixed tiles, rows that
+        // nobody sees or that are not finite become zeros before the product reads them
+        const int t = threadIdx.x - 320;
+        for (int j = 0; j < nt; ++j) {
+          if (!bar_wait_warp(&v_full[j & 1], (j >> 1) & 1)) break;
+          Info* in = info(j);
+          uint8_t* vt = sv + (j & 1) * C::kTile;
+          for (int r = t; r < 128; r += 64) {
+            const int q = r >> 5, bq = in->base[q], kp = bq + (r & 31);
+            if (in->whole[q]) continue;
+            const bool dead = bq == kNowhere || !(kp <= posmax && (kp >= lowmin || kp < sinks));
+            bool bad = false;
+            if (!dead) {
+#pragma unroll
+              for (int ch = 0; ch < D / 8; ++ch) {
+                const uint4 v = *chunk_at(vt, r, ch);
+                const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  bad |= (w4[i] & 0x7F80u) == 0x7F80u || (w4[i] & 0x7F800000u) == 0x7F800000u;
+              }
+              if (bad) atomicOr(&in->poison[q], 1u << (r & 31));
+            }
+            if (dead || bad)
+#pragma unroll
+              for (int ch = 0; ch < D / 8; ++ch) *chunk_at(vt, r, ch) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          mbar_arrive(&v_clean[j & 1]);
+        }
       }
-    } else {
+    } else if (warp < 12) {
       // -------------------------------------------------------------- converting warps, one page of a tile each
       using L = Kv4<D>;
       constexpr int NI = D / 32;     // 16-byte pieces of K (and of V) a lane takes
       constexpr int PR = D / 32;     // pieces of a K row
-      const int w = warp - 9;
-      uint4 kr[NI], vr[NI];
-      uint32_t ksb[NI], vsb[NI];
-      float krow, vrow;
-      int base;
+      const int w = warp - 8;
       // V piece i of this lane: unit of (position pair column j, block, t); the order differs by t so that the
       // lanes' rows fall into different banks
       auto v_unit = [&](int i) {
         if constexpr (D == 128) return ((i + lane) & 3) * 32 + lane;
         return i * 32 + lane;
       };
-      auto fetch = [&](int j) {
-        const int u = 4 * j + w;
-        const int pg = u < pages ? cache_page(c, b, base_at(u) / kKvPage) : -1;
-        base = pg >= 0 ? base_at(u) : kNowhere;
-        krow = vrow = 0.f;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          kr[i] = vr[i] = make_uint4(0u, 0u, 0u, 0u);
-          ksb[i] = vsb[i] = 0;
-        }
-        if (pg < 0) return;
-        const size_t off = ((size_t)pg * c.Hkv + hkv) * L::kBytes;
-        const uint8_t *kp = c.K + off, *vp = c.V + off;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const int e = i * 32 + lane;  // piece: row e / PR, elements 32 (e % PR) ..
-          kr[i] = __ldg(reinterpret_cast<const uint4*>(kp + e * 16));
-          ksb[i] = __ldg(reinterpret_cast<const uint16_t*>(kp + L::kCodes + e * 2));
-          const int v = v_unit(i);
-          vr[i] = __ldg(reinterpret_cast<const uint4*>(vp + v * 16));
-          vsb[i] = __ldg(reinterpret_cast<const uint16_t*>(vp + L::kCodes + (v % (D / 4)) / 4 * kKvPage +
-                                                           8 * (v & 3) + 2 * (v / (D / 4))));
-        }
-        krow = __ldg(reinterpret_cast<const float*>(kp + L::kRows) + lane);
-        vrow = __ldg(reinterpret_cast<const float*>(vp + L::kRows) + lane);
-      };
+      auto v_row = [&](int v) { return 8 * (v & 3) + 2 * (v / (D / 4)); };
+      // a piece's loads go out before the wait for its slot
+      uint4 raw[NI];
+      uint32_t ksb[NI], vsb[NI];
       bool ok = true;
-      if (nt > 0) fetch(0);
+      int page = 0 < pages ? (w < pages ? cache_page(c, b, base_at(w) / kKvPage) : -1) : -1;
       for (int j = 0; j < nt; ++j) {
-        const int s = j & 1;
-        const bool whole = base + kKvPage - 1 <= posmin && (base >= lowmax || base + kKvPage <= sinks);
+        const int s = j & 1, u = 4 * j + w;
+        const int base = page >= 0 ? base_at(u) : kNowhere;
+        const uint8_t* kp = c.K + ((size_t)max(page, 0) * c.Hkv + hkv) * L::kBytes;
+        const uint8_t* vp = c.V + ((size_t)max(page, 0) * c.Hkv + hkv) * L::kBytes;
+        float krow = 0.f, vrow = 0.f;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int e = i * 32 + lane, v = v_unit(i);  // K piece: row e / PR, elements 32 (e % PR) ..
+          raw[i] = make_uint4(0u, 0u, 0u, 0u);
+          ksb[i] = vsb[i] = 0;
+          if (page >= 0) {
+            raw[i] = __ldg(reinterpret_cast<const uint4*>(kp + e * 16));
+            ksb[i] = __ldg(reinterpret_cast<const uint16_t*>(kp + L::kCodes + e * 2));
+            vsb[i] = __ldg(reinterpret_cast<const uint16_t*>(vp + L::kCodes + (v % (D / 4)) / 4 * kKvPage + v_row(v)));
+          }
+        }
+        if (page >= 0) {
+          krow = __ldg(reinterpret_cast<const float*>(kp + L::kRows) + lane);
+          vrow = __ldg(reinterpret_cast<const float*>(vp + L::kRows) + lane);
+        }
+        // the next page's id, two loads ahead of its use
+        const int next = u + 4 < pages ? cache_page(c, b, base_at(u + 4) / kKvPage) : -1;
+        const int whole = quarter_whole(base);
         uint32_t dead = 0, poison = 0;
         if (!whole) {
           const int pos = base + lane;
           dead = __ballot_sync(0xFFFFFFFFu, !(pos <= posmax && (pos >= lowmin || pos < sinks)));
           uint32_t bad = 0;
 #pragma unroll
-          for (int i = 0; i < NI; ++i) {
-            const int v = v_unit(i), r = 8 * (v & 3) + 2 * (v / (D / 4));
-            bad |= (((vsb[i] & 0x7Fu) == 0x7Fu ? 1u : 0u) | ((vsb[i] & 0x7F00u) == 0x7F00u ? 2u : 0u)) << r;
-          }
+          for (int i = 0; i < NI; ++i)
+            bad |= (((vsb[i] & 0x7Fu) == 0x7Fu ? 1u : 0u) | ((vsb[i] & 0x7F00u) == 0x7F00u ? 2u : 0u))
+                   << v_row(v_unit(i));
           poison = __reduce_or_sync(0xFFFFFFFFu, bad) & ~dead;
         }
         Info* in = info(j);
@@ -460,6 +509,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
         if (lane == 0) {
           in->base[w] = base;
           in->poison[w] = poison;
+          in->whole[w] = whole;
         }
         in->ks[w * 32 + lane] = krow * p.scale_log2;
         in->vs[w * 32 + lane] = (dead >> lane) & 1u ? 0.f : vrow;
@@ -467,208 +517,215 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
           const int e = i * 32 + lane, r = w * 32 + e / PR, q = e % PR;
-          const uint32_t words[4] = {kr[i].x, kr[i].y, kr[i].z, kr[i].w};
+          const uint32_t words[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
           const uint32_t s2 = e4m3x2_f16(ksb[i]);
-          uint32_t o[16];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            uint32_t h[4];
+            uint32_t h[4], o[4];
             e2m1x8(words[x], h);
             const uint32_t sd = __byte_perm(s2, 0, x < 2 ? 0x1010 : 0x3232);
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
               const float2 f = scaled(h[y], sd);
-              o[4 * x + y] = pack_bf16(f.x, f.y);
+              o[y] = pack_bf16(f.x, f.y);
             }
+            *chunk_at(kt, r, 4 * q + x) = make_uint4(o[0], o[1], o[2], o[3]);
           }
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            *chunk_at(kt, r, 4 * q + x) = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         mbar_arrive(&k_full[s]);
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+          if (page >= 0) raw[i] = __ldg(reinterpret_cast<const uint4*>(vp + v_unit(i) * 16));
         if (j >= 2 && !(ok = bar_wait_warp(&v_empty[s], ((j >> 1) - 1) & 1))) break;
         uint8_t* vt = sv + s * C::kTile;
         dead |= poison;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-          const int v = v_unit(i), r = 8 * (v & 3) + 2 * (v / (D / 4)), blk = (v % (D / 4)) / 4;
-          const uint32_t words[4] = {vr[i].x, vr[i].y, vr[i].z, vr[i].w};
+          const int v = v_unit(i), r = v_row(v), blk = (v % (D / 4)) / 4, row = w * 32 + r;
+          const uint32_t words[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
           uint32_t sb = vsb[i];
           if ((dead >> r) & 1u) sb &= 0xFF00u;
           if ((dead >> r) & 2u) sb &= 0x00FFu;
           const uint32_t s2 = e4m3x2_f16(sb);
-          uint32_t o0[8], o1[8];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t h[4];
+          for (int x = 0; x < 4; x += 2) {
+            uint32_t h[4], g[4], o0[4], o1[4];
             e2m1x8(words[x], h);
+            e2m1x8(words[x + 1], g);
 #pragma unroll
-            for (int y = 0; y < 4; y += 2) {
-              const float2 f = scaled(h[y], s2), g = scaled(h[y + 1], s2);
-              o0[2 * x + y / 2] = pack_bf16(f.x, g.x);
-              o1[2 * x + y / 2] = pack_bf16(f.y, g.y);
+            for (int y = 0; y < 2; ++y) {
+              const float2 f0 = scaled(h[2 * y], s2), f1 = scaled(h[2 * y + 1], s2);
+              const float2 g0 = scaled(g[2 * y], s2), g1 = scaled(g[2 * y + 1], s2);
+              o0[y] = pack_bf16(f0.x, f1.x);
+              o1[y] = pack_bf16(f0.y, f1.y);
+              o0[2 + y] = pack_bf16(g0.x, g1.x);
+              o1[2 + y] = pack_bf16(g0.y, g1.y);
             }
+            *chunk_at(vt, row, 2 * blk + x / 2) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+            *chunk_at(vt, row + 1, 2 * blk + x / 2) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
           }
-          const int row = w * 32 + r;
-          *chunk_at(vt, row, 2 * blk) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-          *chunk_at(vt, row, 2 * blk + 1) = make_uint4(o0[4], o0[5], o0[6], o0[7]);
-          *chunk_at(vt, row + 1, 2 * blk) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-          *chunk_at(vt, row + 1, 2 * blk + 1) = make_uint4(o1[4], o1[5], o1[6], o1[7]);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         mbar_arrive(&v_full[s]);
-        if (j + 1 < nt) fetch(j + 1);
+        page = next;
       }
       if (!ok && lane == 0) *failed = 1;
     }
+  }
   } else {
-    // ---------------------------------------------------------------- softmax: one pair a thread
-    const int x = warp >> 2, m = threadIdx.x & 127;
+    if constexpr (FMT == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    // ---------------------------------------------------------------- softmax: a warp has 32 pairs (its TMEM
+    // lanes); lane (g, t) holds pairs g, g + 8, g + 16, g + 24 and columns 2 t, 2 t + 1 of every 8
+    const int x = warp >> 2, lg = lane >> 2, lt = lane & 3;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + x * 128 + lanes, t_o = tmem + 256 + x * 128 + lanes;
-    const int col = x * 128 + m, cc = c0 + col;
-    const bool valid = col < ncol;
-    const int pos = valid ? first + cc / G : posmin;
-    const int low = win ? max(0, pos - p.window + 1) : 0;
-    float ref = -INFINITY, l = 0.f;
+    const int col0 = x * 128 + (warp & 3) * 32;   // the warp's first pair
+    int pos[4], low[4];
+    float ref[4], l[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int col = col0 + 8 * k + lg;
+      pos[k] = col < ncol ? first + (c0 + col) / G : posmin;
+      low[k] = win ? max(0, pos[k] - p.window + 1) : 0;
+      ref[k] = -INFINITY;
+      l[k] = 0.f;
+    }
     bool ok = true;
-    int cleanings = 0;
     for (int j = 0; j < nt; ++j) {
       if (!(ok = bar_wait_warp(&s_full[x], j & 1))) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const Info* in = info(j);
-      uint32_t see[4];
-      bool mine = true, tile_whole = true;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int bq = in->base[q];
-        see[q] = sees(bq, pos, low, sinks);
-        mine = mine && see[q] == 0xFFFFFFFFu;
-        tile_whole = tile_whole && bq + kKvPage - 1 <= posmin && (bq >= lowmax || bq + kKvPage <= sinks);
-      }
-      const bool whole = __all_sync(0xFFFFFFFFu, mine ? 1 : 0) != 0;
-      if (FMT == 0 && !tile_whole) {
-        // V rows that nobody sees, or that are not finite: zero (all 256 threads, half a row each)
-        ok = bar_wait_warp(&v_full[j & 1], (j >> 1) & 1);
-        const int r = threadIdx.x >> 1, q = r >> 5;
-        const int bq = in->base[q], kp = bq + (r & 31);
-        uint8_t* vt = sv + (j & 1) * C::kTile;
-        if (ok) {
-          const bool dead = bq == kNowhere || !(kp <= posmax && (kp >= lowmin || kp < sinks));
-          bool bad = false;
-          constexpr int H = D / 16;  // 16-byte chunks of half a row
-#pragma unroll
-          for (int ch = 0; ch < H; ++ch) {
-            const uint4 v = *chunk_at(vt, r, (threadIdx.x & 1) * H + ch);
-            const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              bad |= (w4[i] & 0x7F80u) == 0x7F80u || (w4[i] & 0x7F800000u) == 0x7F800000u;
-          }
-          bad = __shfl_xor_sync(0xFFFFFFFFu, bad ? 1 : 0, 1) || bad;
-          if (dead || bad)
-#pragma unroll
-            for (int ch = 0; ch < H; ++ch)
-              *chunk_at(vt, r, (threadIdx.x & 1) * H + ch) = make_uint4(0u, 0u, 0u, 0u);
-          if (bad && !dead && !(threadIdx.x & 1))
-            atomicOr(const_cast<uint32_t*>(&in->poison[q]), 1u << (r & 31));
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        // the tile's rows are all done when both warpgroups have come here (a wait that ends, unlike a CTA
-        // barrier, should one of them have given up)
-        mbar_arrive(cleaned);
-        ok = bar_wait_warp(cleaned, cleanings++ & 1) && ok;
-        if (!ok) break;
+      const int4 wq = *reinterpret_cast<const int4*>(in->whole);
+      int kind = 0;  // 0: every pair sees every key; 1: a mask; 2: a mask, and V rows that are not finite
+      if (!(wq.x && wq.y && wq.z && wq.w)) {
+        if (FMT == 0 && !(ok = bar_wait_warp(&v_clean[j & 1], (j >> 1) & 1))) break;
+        kind = (in->poison[0] | in->poison[1] | in->poison[2] | in->poison[3]) ? 2 : 1;
       }
       // One pass with the maximum of the tiles before: t = log2 of p, p packed in registers.  If some row's
       // scores exceed it by more than 2^8 (always on its first tile), the scores are still in TMEM: the
       // reference is replaced, O rescaled and the pass taken again.
-      uint32_t pk[4][16];
-      float sum, mx;
+      uint32_t pk[4][2][8];  // [32 keys][16 pairs][register of the store]
+      float sum[4], mx[4];
       auto pass = [&](auto w_) {
-        constexpr bool kWhole = decltype(w_)::value;
-        const float nm = ref == -INFINITY ? 0.f : -ref;
-        const uint64_t nm2 = pair2(nm, nm), sc2 = pair2(p.scale_log2, p.scale_log2);
-        uint64_t sum2 = 0;  // two partial sums
-        mx = -INFINITY;
-        sum = 0.f;
+        constexpr int kKind = decltype(w_)::value;
+        uint64_t nm2[4], sum2[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float nm = ref[k] == -INFINITY ? 0.f : -ref[k];
+          nm2[k] = pair2(nm, nm);
+          sum2[k] = 0;
+          mx[k] = -INFINITY;
+        }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          float s[32];
-          tm_ld32(t_s + q * 32, s);
-          const uint32_t poison = kWhole ? 0u : in->poison[q];
+          uint32_t s[2][16];
+          tm_frag_ld(t_s + q * 32, s[0]);
+          tm_frag_ld(t_s + (16u << 16) + q * 32, s[1]);
+          uint32_t see[4], poison = 0;
+          if constexpr (kKind > 0) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            float4 ks, vs;
+            for (int k = 0; k < 4; ++k) see[k] = sees(in->base[q], pos[k], low[k], sinks) >> (2 * lt);
+            if constexpr (kKind == 2) poison = in->poison[q] >> (2 * lt);
+          }
+          tm_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint64_t ks2, vs2 = 0;
             if constexpr (FMT == 1) {
-              ks = *reinterpret_cast<const float4*>(in->ks + q * 32 + i);
-              vs = *reinterpret_cast<const float4*>(in->vs + q * 32 + i);
+              const float2 a = *reinterpret_cast<const float2*>(in->ks + q * 32 + 8 * i + 2 * lt);
+              const float2 v = *reinterpret_cast<const float2*>(in->vs + q * 32 + 8 * i + 2 * lt);
+              ks2 = pair2(a.x, a.y);
+              vs2 = pair2(v.x, v.y);
+            } else {
+              ks2 = pair2(p.scale_log2, p.scale_log2);
             }
-            float t[4];
 #pragma unroll
-            for (int h = 0; h < 4; h += 2)
-              unpair2(fma2(pair2(s[i + h], s[i + h + 1]),
-                           FMT ? (h ? pair2(ks.z, ks.w) : pair2(ks.x, ks.y)) : sc2, nm2),
-                      t[h], t[h + 1]);
-            if constexpr (!kWhole) {
-#pragma unroll
-              for (int h = 0; h < 4; ++h) t[h] = (see[q] >> (i + h)) & 1u ? t[h] : -INFINITY;
-            }
-            mx = fmaxf(fmaxf(mx, fmaxf(t[0], t[1])), fmaxf(t[2], t[3]));
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              t[h] = ex2f(t[h]);
-              if constexpr (!kWhole) {
-                if ((poison & see[q]) >> (i + h) & 1u) t[h] = __int_as_float(0x7FFFFFFF);
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t* sr = &s[k >> 1][4 * i + 2 * (k & 1)];
+              float t0, t1;
+              unpair2(fma2(pair2(__uint_as_float(sr[0]), __uint_as_float(sr[1])), ks2, nm2[k]), t0, t1);
+              if constexpr (kKind > 0) {
+                t0 = (see[k] >> (8 * i)) & 1u ? t0 : -INFINITY;
+                t1 = (see[k] >> (8 * i)) & 2u ? t1 : -INFINITY;
               }
-            }
-            sum2 = add2(sum2, add2(pair2(t[0], t[1]), pair2(t[2], t[3])));
-            if constexpr (FMT == 1) {
-              const float v4[4] = {vs.x, vs.y, vs.z, vs.w};
-#pragma unroll
-              for (int h = 0; h < 4; ++h) {
-                t[h] *= v4[h];
-                if constexpr (!kWhole) t[h] = (see[q] >> (i + h)) & 1u ? t[h] : 0.f;
+              mx[k] = fmaxf(mx[k], fmaxf(t0, t1));
+              t0 = ex2f(t0);
+              t1 = ex2f(t1);
+              if constexpr (kKind == 2) {
+                if (((see[k] & poison) >> (8 * i)) & 1u) t0 = __int_as_float(0x7FFFFFFF);
+                if (((see[k] & poison) >> (8 * i)) & 2u) t1 = __int_as_float(0x7FFFFFFF);
               }
+              uint64_t t2 = pair2(t0, t1);
+              sum2[k] = add2(sum2[k], t2);
+              if constexpr (FMT == 1) {
+                unpair2(mul2(t2, vs2), t0, t1);
+                if constexpr (kKind > 0) {  // an unseen row's scale may be anything
+                  t0 = (see[k] >> (8 * i)) & 1u ? t0 : 0.f;
+                  t1 = (see[k] >> (8 * i)) & 2u ? t1 : 0.f;
+                }
+              }
+              pk[q][k >> 1][2 * i + (k & 1)] = pack_bf16(t0, t1);
             }
-            pk[q][i / 2] = pack_bf16(t[0], t[1]);
-            pk[q][i / 2 + 1] = pack_bf16(t[2], t[3]);
           }
         }
-        float a, b2;
-        unpair2(sum2, a, b2);
-        sum = a + b2;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float a, b2;
+          unpair2(sum2[k], a, b2);
+          sum[k] = a + b2;
+        }
       };
       auto run_pass = [&]() {
-        if (whole)
-          pass(std::integral_constant<bool, true>{});
+        if (kind == 0)
+          pass(std::integral_constant<int, 0>{});
+        else if (kind == 1)
+          pass(std::integral_constant<int, 1>{});
         else
-          pass(std::integral_constant<bool, false>{});
+          pass(std::integral_constant<int, 2>{});
       };
       run_pass();
-      const bool grow = ref == -INFINITY ? mx > -INFINITY : mx > kGrow;
+      bool grow = false;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) grow |= ref[k] == -INFINITY ? mx[k] > -INFINITY : mx[k] > kGrow;
       if (__any_sync(0xFFFFFFFFu, grow)) {
-        const float alpha = !grow || ref == -INFINITY ? 1.f : ex2f(-mx);
-        if (grow) {
-          l *= alpha;
-          ref = ref == -INFINITY ? mx : ref + mx;
+        float alpha[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float m = mx[k];
+          m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+          m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+          alpha[k] = 1.f;
+          if (ref[k] == -INFINITY) {
+            ref[k] = m;
+          } else if (m > kGrow) {
+            alpha[k] = ex2f(-m);
+            ref[k] += m;
+          }
+          l[k] *= alpha[k];
         }
         if (j > 0) {  // the product with the previous tile is done (s_full)
 #pragma unroll 1
-          for (int d = 0; d < D; d += 32) {
-            float t[32];
-            tm_ld32(t_o + d, t);
+          for (int d = 0; d < 2 * D; d += 32) {
+            const uint32_t at = t_o + (d >= D ? (16u << 16) + d - D : d);
+            const float a0 = d >= D ? alpha[2] : alpha[0], a1 = d >= D ? alpha[3] : alpha[1];
+            uint32_t r[16];
+            tm_frag_ld(at, r);
+            tm_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) t[i] *= alpha;
-            tm_st32(t_o + d, t);
+            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * (i & 2 ? a1 : a0));
+            tm_frag_st(at, r);
           }
         }
         run_pass();
       }
-      l += sum;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) tm_st16(t_s + q * 16, pk[q]);
+      for (int k = 0; k < 4; ++k) l[k] += sum[k];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        tm_pair_st(t_s + q * 16, pk[q][0]);
+        tm_pair_st(t_s + (16u << 16) + q * 16, pk[q][1]);
+      }
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       mbar_arrive(&p_full[x]);
@@ -676,7 +733,19 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
     if (ok && nt > 0) ok = bar_wait_warp(&o_done[x], 0);
     if (ok) {
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const float inv = 1.f / l;
+      // the sums of this lane's own row (pair `lane` of the warp), whose outputs it stores
+      float total = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float v = l[k];
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+        v = __shfl_sync(0xFFFFFFFFu, v, (lane & 7) * 4);
+        if ((lane >> 3) == k) total = v;
+      }
+      const float inv = 1.f / total;
+      const int col = col0 + lane, cc = c0 + col;
+      const bool valid = col < ncol;
       uint16_t* dst = static_cast<uint16_t*>(p.out) + (size_t)(sq.r0 + cc / G) * p.out_stride +
                       (size_t)(hkv * G + cc % G) * D;
 #pragma unroll 1
@@ -691,7 +760,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
         if (valid) {
           uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = l == 0.f ? 0u : pack_bf16(t[2 * i] * inv, t[2 * i + 1] * inv);
+          for (int i = 0; i < 16; ++i) w[i] = total == 0.f ? 0u : pack_bf16(t[2 * i] * inv, t[2 * i + 1] * inv);
           if ((reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
@@ -713,7 +782,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   if (threadIdx.x == 0 && *failed) cache_flag(c, TF_CACHE_TIMEOUT);
-  if (warp == 8) {
+  if (warp == C::kMmaWarp) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols) : "memory");
   }
