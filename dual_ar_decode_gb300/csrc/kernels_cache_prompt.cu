@@ -19,8 +19,8 @@
 //   * bf16 pages come by TMA (128-byte swizzle).  4-bit pages are converted by
 //     four warps: e2m1 x e4m3 has at most 6 significant bits and is exact in bf16;
 //     K's row scale multiplies the scores and V's the probabilities, in float32.
-//   * The maximum is replaced, and O rescaled in TMEM, only when a score exceeds
-//     it by more than 2^8.  Probabilities enter as bf16 (half a step: 2^-8 of
+//   * The maximum is replaced, and O rescaled in TMEM, only when the probabilities
+//     relative to it grow past 2^13.  Probabilities enter as bf16 (half a step: 2^-8 of
 //     each, as much as the output's own rounding); their sum is of the unrounded
 //     ones, in float32.
 //   * Tiles that some row does not see whole are masked, and V rows that no row
@@ -44,7 +44,9 @@ namespace tf {
 
 namespace {
 
-constexpr float kGrow = 8.0f;    // log2 of the growth at which the maximum is replaced
+// The maximum that the exponentials are relative to is replaced when a lane's sum of a row's 32 probabilities of
+// a tile exceeds this (2^13; so no probability does).
+constexpr float kMaxSum = 8192.0f;
 constexpr int kInfo = 4;         // tiles of which the position / scale records are kept
 constexpr int kNowhere = 0x3FFFFFFF;  // base position of a quarter that holds nothing
 
@@ -240,7 +242,8 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
   uint8_t* sv = smem + C::kOffV;
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t *k_full = bar, *k_empty = bar + 2, *v_full = bar + 4, *v_empty = bar + 6;  // [2] each
-  uint64_t *s_full = bar + 8, *p_full = bar + 10, *o_done = bar + 12, *drained = bar + 14, *v_clean = bar + 18;  // v_clean [2]
+  uint64_t *s_full = bar + 8, *p_full = bar + 10, *o_done = bar + 12, *drained = bar + 14, *q_full = bar + 15;
+  uint64_t* v_clean = bar + 18;  // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 16);
   volatile uint32_t* failed = tmem_slot + 1;
 
@@ -287,6 +290,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
       mbar_init(&o_done[i], 1);
     }
     mbar_init(drained, 1);
+    mbar_init(q_full, 256);
     *failed = 0;
     fence_mbar_init();
   }
@@ -296,25 +300,6 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  // Q: pair m of the CTA is row (c0 + m) / G, head (c0 + m) % G; rows past the last pair are zero.
-  for (int e = threadIdx.x; e < 256 * (D / 8); e += C::kThreads) {
-    const int m = e / (D / 8), ch = e % (D / 8), cc = c0 + m;
-    uint4* dst = chunk_at(smem + (m >> 7) * C::kTile, m & 127, ch);
-    const uint16_t* src = static_cast<const uint16_t*>(p.q) + (size_t)(sq.r0 + cc / G) * p.q_stride +
-                          (size_t)(hkv * G + cc % G) * D + ch * 8;
-    if (m >= ncol) {
-      *dst = make_uint4(0u, 0u, 0u, 0u);
-    } else if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-    } else {
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = src[2 * i] | static_cast<uint32_t>(src[2 * i + 1]) << 16;
-      *dst = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -338,7 +323,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
         mma_commit(&s_full[x]);
       };
       if (nt > 0) {
-        ok = bar_wait(&k_full[0], 0);
+        ok = bar_wait(q_full, 0) && bar_wait(&k_full[0], 0);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         if (ok) {
           score(0, 0);
@@ -581,6 +566,26 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + x * 128 + lanes, t_o = tmem + 256 + x * 128 + lanes;
     const int col0 = x * 128 + (warp & 3) * 32;   // the warp's first pair
+    // Q (by these 256 threads): pair m of the CTA is row (c0 + m) / G, head (c0 + m) % G; rows past the last pair are zero.
+    for (int e = threadIdx.x; e < 256 * (D / 8); e += 256) {
+      const int m = e / (D / 8), ch = e % (D / 8), cc = c0 + m;
+      uint4* dst = chunk_at(smem + (m >> 7) * C::kTile, m & 127, ch);
+      const uint16_t* src = static_cast<const uint16_t*>(p.q) + (size_t)(sq.r0 + cc / G) * p.q_stride +
+                            (size_t)(hkv * G + cc % G) * D + ch * 8;
+      if (m >= ncol) {
+        *dst = make_uint4(0u, 0u, 0u, 0u);
+      } else if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = src[2 * i] | static_cast<uint32_t>(src[2 * i + 1]) << 16;
+        *dst = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    mbar_arrive(q_full);
     int pos[4], low[4];
     float ref[4], l[4];
 #pragma unroll
@@ -602,11 +607,15 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
         if (FMT == 0 && !(ok = bar_wait_warp(&v_clean[j & 1], (j >> 1) & 1))) break;
         kind = (in->poison[0] | in->poison[1] | in->poison[2] | in->poison[3]) ? 2 : 1;
       }
-      // One pass with the maximum of the tiles before: t = log2 of p, p packed in registers.  If some row's
-      // scores exceed it by more than 2^8 (always on its first tile), the scores are still in TMEM: the
-      // reference is replaced, O rescaled and the pass taken again.
+      // One pass relative to the maximum of the tiles before, p packed in registers.  On a row's first tile, or
+      // when a sum comes out too large, the scores (still in TMEM) give a new maximum, O is rescaled and the pass
+      // taken (again).
       uint32_t pk[4][2][8];  // [32 keys][16 pairs][register of the store]
-      float sum[4], mx[4];
+      float sum[4];
+      auto masks = [&](int q, uint32_t (&see)[4]) {  // bits 8 i + e: columns 8 i + 2 t + e of the quarter
+#pragma unroll
+        for (int k = 0; k < 4; ++k) see[k] = sees(in->base[q], pos[k], low[k], sinks) >> (2 * lt);
+      };
       auto pass = [&](auto w_) {
         constexpr int kKind = decltype(w_)::value;
         uint64_t nm2[4], sum2[4];
@@ -615,51 +624,48 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
           const float nm = ref[k] == -INFINITY ? 0.f : -ref[k];
           nm2[k] = pair2(nm, nm);
           sum2[k] = 0;
-          mx[k] = -INFINITY;
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t s[2][16];
           tm_frag_ld(t_s + q * 32, s[0]);
           tm_frag_ld(t_s + (16u << 16) + q * 32, s[1]);
+          float2 ks[FMT ? 4 : 1], vs[FMT ? 4 : 1];
+          if constexpr (FMT == 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              ks[i] = *reinterpret_cast<const float2*>(in->ks + q * 32 + 8 * i + 2 * lt);
+              vs[i] = *reinterpret_cast<const float2*>(in->vs + q * 32 + 8 * i + 2 * lt);
+            }
+          }
           uint32_t see[4], poison = 0;
           if constexpr (kKind > 0) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) see[k] = sees(in->base[q], pos[k], low[k], sinks) >> (2 * lt);
+            masks(q, see);
             if constexpr (kKind == 2) poison = in->poison[q] >> (2 * lt);
           }
           tm_wait_ld();
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint64_t ks2, vs2 = 0;
-            if constexpr (FMT == 1) {
-              const float2 a = *reinterpret_cast<const float2*>(in->ks + q * 32 + 8 * i + 2 * lt);
-              const float2 v = *reinterpret_cast<const float2*>(in->vs + q * 32 + 8 * i + 2 * lt);
-              ks2 = pair2(a.x, a.y);
-              vs2 = pair2(v.x, v.y);
-            } else {
-              ks2 = pair2(p.scale_log2, p.scale_log2);
-            }
+            const uint64_t ks2 = FMT ? pair2(ks[FMT ? i : 0].x, ks[FMT ? i : 0].y) : pair2(p.scale_log2, p.scale_log2);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t* sr = &s[k >> 1][4 * i + 2 * (k & 1)];
               float t0, t1;
               unpair2(fma2(pair2(__uint_as_float(sr[0]), __uint_as_float(sr[1])), ks2, nm2[k]), t0, t1);
-              if constexpr (kKind > 0) {
-                t0 = (see[k] >> (8 * i)) & 1u ? t0 : -INFINITY;
-                t1 = (see[k] >> (8 * i)) & 2u ? t1 : -INFINITY;
-              }
-              mx[k] = fmaxf(mx[k], fmaxf(t0, t1));
               t0 = ex2f(t0);
               t1 = ex2f(t1);
+              if constexpr (kKind > 0) {
+                t0 = (see[k] >> (8 * i)) & 1u ? t0 : 0.f;
+                t1 = (see[k] >> (8 * i)) & 2u ? t1 : 0.f;
+              }
               if constexpr (kKind == 2) {
                 if (((see[k] & poison) >> (8 * i)) & 1u) t0 = __int_as_float(0x7FFFFFFF);
                 if (((see[k] & poison) >> (8 * i)) & 2u) t1 = __int_as_float(0x7FFFFFFF);
               }
-              uint64_t t2 = pair2(t0, t1);
+              const uint64_t t2 = pair2(t0, t1);
               sum2[k] = add2(sum2[k], t2);
               if constexpr (FMT == 1) {
-                unpair2(mul2(t2, vs2), t0, t1);
+                unpair2(mul2(t2, pair2(vs[FMT ? i : 0].x, vs[FMT ? i : 0].y)), t0, t1);
                 if constexpr (kKind > 0) {  // an unseen row's scale may be anything
                   t0 = (see[k] >> (8 * i)) & 1u ? t0 : 0.f;
                   t1 = (see[k] >> (8 * i)) & 2u ? t1 : 0.f;
@@ -676,48 +682,70 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
           sum[k] = a + b2;
         }
       };
-      auto run_pass = [&]() {
+      bool again = false;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) again |= ref[k] == -INFINITY;
+      again = __any_sync(0xFFFFFFFFu, again);
+      for (int round = 0; round < 2; ++round) {
+        if (again) {
+          float mx[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx[k] = -INFINITY;
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t s[2][16], see[4];
+            tm_frag_ld(t_s + q * 32, s[0]);
+            tm_frag_ld(t_s + (16u << 16) + q * 32, s[1]);
+            masks(q, see);
+            tm_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float2 ks = make_float2(p.scale_log2, p.scale_log2);
+              if constexpr (FMT == 1) ks = *reinterpret_cast<const float2*>(in->ks + q * 32 + 8 * i + 2 * lt);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t* sr = &s[k >> 1][4 * i + 2 * (k & 1)];
+                if ((see[k] >> (8 * i)) & 1u) mx[k] = fmaxf(mx[k], __uint_as_float(sr[0]) * ks.x);
+                if ((see[k] >> (8 * i)) & 2u) mx[k] = fmaxf(mx[k], __uint_as_float(sr[1]) * ks.y);
+              }
+            }
+          }
+          float alpha[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float m = mx[k];
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+            alpha[k] = 1.f;
+            if (m > ref[k]) {
+              if (ref[k] != -INFINITY) alpha[k] = ex2f(ref[k] - m);
+              ref[k] = m;
+            }
+            l[k] *= alpha[k];
+          }
+          if (j > 0) {  // the product with the previous tile is done (s_full)
+#pragma unroll 1
+            for (int d = 0; d < 2 * D; d += 32) {
+              const uint32_t at = t_o + (d >= D ? (16u << 16) + d - D : d);
+              const float a0 = d >= D ? alpha[2] : alpha[0], a1 = d >= D ? alpha[3] : alpha[1];
+              uint32_t r[16];
+              tm_frag_ld(at, r);
+              tm_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * (i & 2 ? a1 : a0));
+              tm_frag_st(at, r);
+            }
+          }
+        }
         if (kind == 0)
           pass(std::integral_constant<int, 0>{});
         else if (kind == 1)
           pass(std::integral_constant<int, 1>{});
         else
           pass(std::integral_constant<int, 2>{});
-      };
-      run_pass();
-      bool grow = false;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) grow |= ref[k] == -INFINITY ? mx[k] > -INFINITY : mx[k] > kGrow;
-      if (__any_sync(0xFFFFFFFFu, grow)) {
-        float alpha[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float m = mx[k];
-          m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-          m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-          alpha[k] = 1.f;
-          if (ref[k] == -INFINITY) {
-            ref[k] = m;
-          } else if (m > kGrow) {
-            alpha[k] = ex2f(-m);
-            ref[k] += m;
-          }
-          l[k] *= alpha[k];
-        }
-        if (j > 0) {  // the product with the previous tile is done (s_full)
-#pragma unroll 1
-          for (int d = 0; d < 2 * D; d += 32) {
-            const uint32_t at = t_o + (d >= D ? (16u << 16) + d - D : d);
-            const float a0 = d >= D ? alpha[2] : alpha[0], a1 = d >= D ? alpha[3] : alpha[1];
-            uint32_t r[16];
-            tm_frag_ld(at, r);
-            tm_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * (i & 2 ? a1 : a0));
-            tm_frag_st(at, r);
-          }
-        }
-        run_pass();
+        again = sum[0] > kMaxSum || sum[1] > kMaxSum || sum[2] > kMaxSum || sum[3] > kMaxSum;
+        if (!__any_sync(0xFFFFFFFFu, again)) break;
+        again = true;
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) l[k] += sum[k];
@@ -743,11 +771,11 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
         v = __shfl_sync(0xFFFFFFFFu, v, (lane & 7) * 4);
         if ((lane >> 3) == k) total = v;
       }
-      const float inv = 1.f / total;
-      const int col = col0 + lane, cc = c0 + col;
-      const bool valid = col < ncol;
-      uint16_t* dst = static_cast<uint16_t*>(p.out) + (size_t)(sq.r0 + cc / G) * p.out_stride +
-                      (size_t)(hkv * G + cc % G) * D;
+      const float inv = total == 0.f ? 0.f : 1.f / total;
+      // Rows go out through the warp's 32 rows of the Q tile (every product that read it is done), so that a
+      // store covers whole rows.
+      uint8_t* mine = smem + x * C::kTile;
+      const int r0 = (warp & 3) * 32;
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {
         float t[32];
@@ -757,23 +785,34 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) t[i] = 0.f;
         }
-        if (valid) {
-          uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = total == 0.f ? 0u : pack_bf16(t[2 * i] * inv, t[2 * i + 1] * inv);
+        for (int i = 0; i < 32; i += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            w[h] = total == 0.f ? 0u : pack_bf16(t[i + 2 * h] * inv, t[i + 2 * h + 1] * inv);
+          *chunk_at(mine, r0 + lane, (d + i) / 8) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      __syncwarp();
+#pragma unroll 4
+      for (int e = lane; e < 32 * (D / 8); e += 32) {
+        const int r = e / (D / 8), ch = e % (D / 8), col = col0 + r, cc = c0 + col;
+        const uint4 v = *chunk_at(mine, r0 + r, ch);
+        if (col < ncol) {
+          uint16_t* dst = static_cast<uint16_t*>(p.out) + (size_t)(sq.r0 + cc / G) * p.out_stride +
+                          (size_t)(hkv * G + cc % G) * D + ch * 8;
           if ((reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
-#pragma unroll
-            for (int i = 0; i < 16; i += 4)
-              *reinterpret_cast<uint4*>(dst + d + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+            *reinterpret_cast<uint4*>(dst) = v;
           } else {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              dst[d + 2 * i] = static_cast<uint16_t>(w[i]);
-              dst[d + 2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
+            for (int i = 0; i < 4; ++i) {
+              dst[2 * i] = static_cast<uint16_t>(w[i]);
+              dst[2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
             }
           }
         }
-        __syncwarp();
       }
     } else if (lane == 0) {
       *failed = 1;
