@@ -409,13 +409,19 @@ __global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
     const uint8_t* Vs = Ks + C::kHalf;
     if (have) {
       // ---- scores: S[key][col]; block bt: keys key_of(bt)
-      float sc[NT][KB / 2][4];
+      // float32 rows: the tensor core truncates when it adds to its accumulator, so long chains drift.  The
+      // leading parts of even and odd steps and the small parts have accumulators of their own, added once.
+      constexpr int kAcc = F32 ? 3 : 1;
+      float sc[NT][KB / 2][4], sx[NT][KB / 2][kAcc][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < KB / 2; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[n][i][e] = 0.f;
+          for (int a = 0; a < kAcc; ++a)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sx[n][i][a][e] = 0.f;
+      auto acc_of = [](int q, int step) { return F32 ? (q > 0 ? 2 : step & 1) : 0; };
       // position in the page of this lane's key of block bt
       auto key_of = [&](int bt) { return FMT ? 8 * (lg >> 1) + 2 * bt + (lg & 1) : 8 * bt + lg; };
       if constexpr (FMT == 1) {
@@ -450,7 +456,7 @@ __global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
                 const uint2 bq = qf[((n * C::kQp + q) * C::kSteps + 2 * w + st) * 32];
 #pragma unroll
                 for (int i = 0; i < KB / 2; ++i)
-                  mma16816<1>(sc[n][i], a[2 * i][2 * st], a[2 * i + 1][2 * st], a[2 * i][2 * st + 1],
+                  mma16816<1>(sx[n][i][acc_of(q, st)], a[2 * i][2 * st], a[2 * i + 1][2 * st], a[2 * i][2 * st + 1],
                               a[2 * i + 1][2 * st + 1], bq.x, bq.y);
               }
         }
@@ -467,10 +473,19 @@ __global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
 #pragma unroll
             for (int q = 0; q < C::kQp; ++q) {
               const uint2 bq = qf[((n * C::kQp + q) * C::kSteps + s) * 32];
-              mma16816<0>(sc[n][0], a[0], a[1], a[2], a[3], bq.x, bq.y);
+              mma16816<0>(sx[n][0][acc_of(q, s)], a[0], a[1], a[2], a[3], bq.x, bq.y);
             }
         }
       }
+
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < KB / 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            sc[n][i][e] = F32 ? (sx[n][i][0][e] + sx[n][i][kAcc > 1 ? 1 : 0][e]) + sx[n][i][kAcc - 1][e]
+                              : sx[n][i][0][e];
 
       // Does every column see every key of the stage?  Else: mask, and keep what no column sees (and
       // infinities and NaN that only some see) out of the second product.
@@ -627,7 +642,8 @@ __global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
 #pragma unroll
           for (int q = 0; q < C::kPp; ++q) pb[n][q][bt] = movmatrix(part[q]);
         }
-      // ---- O^T += V^T P^T
+      // ---- O^T += V^T P^T (float32 rows: a stage's products from zero, small parts first, then one rounded
+      // addition)
       if constexpr (FMT == 1) {
         uint32_t vw[KB][D / 32], vs[KB];
         const int blk = D == 128 ? lg : lg >> 1;
@@ -665,12 +681,20 @@ __global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
           for (int st = 0; st < 2; ++st)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
+            {
+              float t[4] = {0.f, 0.f, 0.f, 0.f};
+              float(&to)[4] = F32 ? t : o[n][2 * w + st];
 #pragma unroll
-              for (int q = 0; q < C::kPp; ++q)
+              for (int q = C::kPp - 1; q >= 0; --q)
 #pragma unroll
                 for (int i = 0; i < KB / 2; ++i)
-                  mma16816<1>(o[n][2 * w + st], a[2 * i][2 * st], a[2 * i][2 * st + 1], a[2 * i + 1][2 * st],
+                  mma16816<1>(to, a[2 * i][2 * st], a[2 * i][2 * st + 1], a[2 * i + 1][2 * st],
                               a[2 * i + 1][2 * st + 1], pb[n][q][2 * i], pb[n][q][2 * i + 1]);
+              if constexpr (F32) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][2 * w + st][e] += t[e];
+              }
+            }
         }
       } else {
         const uint32_t vb = smem_u32(Vs);
@@ -690,10 +714,17 @@ __global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
             a[3] &= keep1;
           }
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NT; ++n) {
+            float t[4] = {0.f, 0.f, 0.f, 0.f};
+            float(&to)[4] = F32 ? t : o[n][i];
 #pragma unroll
-            for (int q = 0; q < C::kPp; ++q)
-              mma16816<0>(o[n][i], a[0], a[1], a[2], a[3], pb[n][q][0], pb[n][q][1]);
+            for (int q = C::kPp - 1; q >= 0; --q)
+              mma16816<0>(to, a[0], a[1], a[2], a[3], pb[n][q][0], pb[n][q][1]);
+            if constexpr (F32) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[n][i][e] += t[e];
+            }
+          }
         }
       }
     }
