@@ -1,6 +1,6 @@
 // Cache operators (sm_103a): rows appended to and read from a paged KV cache
 // in bfloat16 or 4 bits, and page copies.
-#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -18,7 +18,7 @@ namespace {
 // Half a warp takes one row of one head (D / 16 elements a lane), the two
 // halves of a warp the even and the odd position of a pair: a byte of V's
 // codes holds both positions of a pair, so one warp writes it whole.
-constexpr int kRowThreads = 128;
+constexpr int kRowThreads = 128, kReadThreads = 256;
 
 template <int E>
 __device__ __forceinline__ void load_row(const void* base, size_t off, int f32, float (&x)[E]) {
@@ -65,8 +65,19 @@ __device__ __forceinline__ void store_row(void* base, size_t off, int f32, const
     }
   } else {
     uint16_t* p = static_cast<uint16_t*>(base) + off;
+    uint32_t w[E / 2];
 #pragma unroll
-    for (int i = 0; i < E; ++i) p[i] = f32_to_bf16(x[i]);
+    for (int i = 0; i < E / 2; ++i)
+      w[i] = static_cast<uint32_t>(f32_to_bf16(x[2 * i])) | static_cast<uint32_t>(f32_to_bf16(x[2 * i + 1])) << 16;
+    if ((reinterpret_cast<uintptr_t>(p) & (E * 2 - 1)) == 0) {
+      if constexpr (E == 8)
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+      else
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) p[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+    }
   }
 }
 
@@ -79,23 +90,16 @@ __device__ __forceinline__ float half_max_nan(float v, int from, int to) {
   return v;
 }
 
-// e2m1 code of r in [-6, 6]: round to nearest, ties to the even code.
-__device__ __forceinline__ uint32_t e2m1_code(float r) {
-  const float a = fabsf(r);
-  const uint32_t m = (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) + (a >= 3.5f) + (a > 5.0f);
-  return m | (r < 0.0f ? 8u : 0u);
+// Two floats -> two e2m1 codes in a byte (the first in the low nibble): round to nearest even, +-6 at most.
+__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+  uint16_t d;
+  asm("{.reg .b8 b; cvt.rn.satfinite.e2m1x2.f32 b, %1, %2; mov.b16 %0, {b, 0};}" : "=h"(d) : "f"(hi), "f"(lo));
+  return d;
 }
 
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-  const uint32_t m = c & 7u;
-  const float a = m < 2 ? 0.5f * m : __uint_as_float((126u + (m >> 1)) << 23 | (m & 1u) << 22);
-  return (c & 8u) ? -a : a;
-}
-
-// x: a lane's E elements of a row.  Quantises them: codes (one per element),
-// the block's scale byte, the row's scale.
+// x: a lane's E elements of a row.  Quantises them: codes (two per byte), the block's scale byte, the row's scale.
 template <int E>
-__device__ __forceinline__ void quantise_row(const float (&x)[E], uint32_t (&code)[E], uint32_t& sb, float& s) {
+__device__ __forceinline__ void quantise_row(const float (&x)[E], uint32_t (&code)[E / 2], uint32_t& sb, float& s) {
   float am = 0.f;
   bool bad = false;
 #pragma unroll
@@ -115,8 +119,22 @@ __device__ __forceinline__ void quantise_row(const float (&x)[E], uint32_t (&cod
     step = __fmul_rn(e4m3_value(sb), s);
   }
 #pragma unroll
-  for (int i = 0; i < E; ++i)
-    code[i] = step > 0.f ? e2m1_code(fminf(fmaxf(__fdiv_rn(x[i], step), -6.0f), 6.0f)) : 0u;
+  for (int i = 0; i < E / 2; ++i) code[i] = 0;
+  if (!(step > 0.f)) return;
+  // The code is that of the rounded quotient x / step.  x * (1 / step) is within 2^-21 of it (two roundings and
+  // the reciprocal's); where both ends of that interval have the same code, it is the quotient's (rounding is
+  // monotonic), and only the few others need the division.
+  const float inv = __fdiv_rn(1.0f, step);
+  const bool safe = step > 1e-30f && step < 1e30f;
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    const float a = x[2 * i] * inv, b = x[2 * i + 1] * inv;
+    constexpr float kUp = 1.0f + 4.76837158e-7f, kDown = 1.0f - 4.76837158e-7f;
+    const uint32_t c0 = e2m1x2(a * kDown + 0.f, b * kDown + 0.f), c1 = e2m1x2(a * kUp + 0.f, b * kUp + 0.f);
+    code[i] = c0;
+    if (c0 != c1 || !safe)
+      code[i] = e2m1x2(__fdiv_rn(x[2 * i], step) + 0.f, __fdiv_rn(x[2 * i + 1], step) + 0.f);  // + 0: no -0
+  }
 }
 
 // Grid: (position pairs * KV heads, 2 (K, V), sequences); 4 warps a CTA.
@@ -160,7 +178,7 @@ __global__ void __launch_bounds__(kRowThreads) k_cache_append(const CacheRowsPar
     }
   } else {
     uint8_t* head = pool + ((size_t)page * c.Hkv + g) * L::kBytes;
-    uint32_t code[E], sb;
+    uint32_t code[E / 2], sb;
     float s;
     quantise_row<E>(x, code, sb, s);
     if (mine && l == 0) reinterpret_cast<float*>(head + L::kRows)[r] = s;
@@ -170,7 +188,7 @@ __global__ void __launch_bounds__(kRowThreads) k_cache_append(const CacheRowsPar
     if (!isv) {
       uint32_t w = 0;
 #pragma unroll
-      for (int i = 0; i < E; ++i) w |= code[i] << (4 * i);
+      for (int i = 0; i < E / 2; ++i) w |= code[i] << (8 * i);
       if (mine) {
         if constexpr (E == 8)
           *reinterpret_cast<uint32_t*>(head + r * (D / 2) + l * 4) = w;
@@ -186,7 +204,10 @@ __global__ void __launch_bounds__(kRowThreads) k_cache_append(const CacheRowsPar
       for (int w = 0; w < E / 4; ++w) {
         uint32_t v = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v |= code[4 * w + i] << (8 * i);
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t two = code[2 * w + i];
+          v |= ((two & 15u) | (two >> 4) << 8) << (16 * i);
+        }
         const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, v, 16);
         if (both) {
           if (half == 0) dst[w] = v | (o << 4);
@@ -198,46 +219,90 @@ __global__ void __launch_bounds__(kRowThreads) k_cache_append(const CacheRowsPar
   }
 }
 
-// Value of a lane's E elements (from l * E) of position r of a 4-bit page.
-template <int D, int E>
-__device__ __forceinline__ void kv4_row(const uint8_t* head, int isv, int r, int l, float (&x)[E]) {
-  using L = Kv4<D>;
-  const int blk = l * E / 16;
-  const float sc = e4m3_value(head[L::kCodes + (isv ? blk * kKvPage + r : r * (D / 16) + blk)]);
-  const float s = reinterpret_cast<const float*>(head + L::kRows)[r];
+// Four bytes of e2m1 pairs -> f16x2 each (low nibble in the low half).
+__device__ __forceinline__ void e2m1x8_f16(uint32_t v, __half2 (&h)[4]) {
+  uint32_t o[4];
+  asm("{.reg .b8 b0, b1, b2, b3; mov.b32 {b0, b1, b2, b3}, %4;"
+      " cvt.rn.f16x2.e2m1x2 %0, b0; cvt.rn.f16x2.e2m1x2 %1, b1;"
+      " cvt.rn.f16x2.e2m1x2 %2, b2; cvt.rn.f16x2.e2m1x2 %3, b3;}"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+      : "r"(v));
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const int d = l * E + i;
-    const uint32_t by = isv ? head[L::v_byte(r, d)] : head[r * (D / 2) + d / 2];
-    x[i] = e2m1_value(by >> (4 * ((isv ? r : d) & 1)) & 15u) * sc * s;
-  }
+  for (int i = 0; i < 4; ++i) h[i] = *reinterpret_cast<const __half2*>(&o[i]);
 }
 
-// Grid: (rows of a sequence * KV heads / 8, 2 (K, V), sequences).
+// Grid: (position pairs of a sequence * KV heads / 16, 2 (K, V), sequences): half a warp takes a pair of positions
+// of one head, E elements of both a lane, so V's codes (two positions in a byte) are read once.
 template <int D, int FMT>
-__global__ void __launch_bounds__(kRowThreads) k_cache_read(const CacheRowsParams p) {
+__global__ void __launch_bounds__(kReadThreads) k_cache_read(const CacheRowsParams p) {
   constexpr int E = D / 16;
+  using L = Kv4<D>;
   const CacheBatch& c = p.c;
   const int b = blockIdx.z, isv = blockIdx.y;
   const int l = threadIdx.x & 15;
   const SeqRows sq = cache_seq(c, b);
-  const int item = blockIdx.x * (kRowThreads / 16) + (threadIdx.x >> 4);
-  const int i = item / c.Hkv, g = item % c.Hkv;
-  if (i >= sq.n) return;
-  const int pos = sq.len - sq.n + i;
-  float x[E];
+  const int item = blockIdx.x * (kReadThreads / 16) + (threadIdx.x >> 4);
+  const int g = item % c.Hkv, first = sq.len - sq.n;
+  // an even position, the first one at or below `first` (which may be negative)
+  const int base = (first & ~1) + 2 * (item / c.Hkv);
+  if (sq.n == 0 || base >= sq.len) return;
+  float x[2][E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) x[e] = 0.f;
-  const int page = pos < 0 ? -1 : cache_page(c, b, pos / kKvPage);
+  for (int e = 0; e < E; ++e) x[0][e] = x[1][e] = 0.f;
+  const int page = base < 0 ? -1 : cache_page(c, b, base / kKvPage);
   if (page >= 0) {
-    const uint8_t* pool = isv ? c.V : c.K;
-    const int r = pos % kKvPage;
-    if constexpr (FMT == 0)
-      load_row<E>(pool, (((size_t)page * c.Hkv + g) * kKvPage + r) * D + l * E, 0, x);
-    else
-      kv4_row<D, E>(pool + ((size_t)page * c.Hkv + g) * Kv4<D>::kBytes, isv, r, l, x);
+    const int r = base % kKvPage;
+    const uint8_t* head = (isv ? c.V : c.K) + ((size_t)page * c.Hkv + g) * (FMT ? L::kBytes : kKvPage * D * 2);
+    if constexpr (FMT == 0) {
+      load_row<E>(head, r * D + l * E, 0, x[0]);
+      load_row<E>(head, (r + 1) * D + l * E, 0, x[1]);
+    } else {
+      const int blk = l * E / 16;
+      const float2 s = *reinterpret_cast<const float2*>(head + L::kRows + r * 4);
+      const uint8_t* sb = head + L::kCodes + (isv ? blk * kKvPage + r : r * (D / 16) + blk);
+      const float s0 = e4m3_value(sb[0]), s1 = e4m3_value(sb[isv ? 1 : D / 16]);
+      // (e2m1 * b is exact, so the row scale's product is the one rounding)
+      if (isv) {
+        uint32_t w[E / 4];
+        if constexpr (E == 8)
+          *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(head + L::v_byte(r, l * E));
+        else
+          w[0] = *reinterpret_cast<const uint32_t*>(head + L::v_byte(r, l * E));
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) {
+          __half2 h[4];
+          e2m1x8_f16(w[i], h);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float2 f = __half22float2(h[y]);
+            x[0][4 * i + y] = f.x * s0 * s.x;
+            x[1][4 * i + y] = f.y * s1 * s.y;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          uint32_t w;
+          if constexpr (E == 8)
+            w = *reinterpret_cast<const uint32_t*>(head + (r + y) * (D / 2) + l * 4);
+          else
+            w = *reinterpret_cast<const uint16_t*>(head + (r + y) * (D / 2) + l * 2);
+          __half2 h[4];
+          e2m1x8_f16(w, h);
+#pragma unroll
+          for (int i = 0; i < E / 2; ++i) {
+            const float2 f = __half22float2(h[i]);
+            x[y][2 * i] = f.x * (y ? s1 : s0) * (y ? s.y : s.x);
+            x[y][2 * i + 1] = f.y * (y ? s1 : s0) * (y ? s.y : s.x);
+          }
+        }
+      }
+    }
   }
-  store_row<E>(isv ? p.v : p.k, (size_t)(sq.r0 + i) * p.stride + (size_t)g * D + l * E, p.f32, x);
+#pragma unroll
+  for (int y = 0; y < 2; ++y)
+    if (base + y >= first && base + y < sq.len)
+      store_row<E>(isv ? p.v : p.k, (size_t)(sq.r0 + base + y - first) * p.stride + (size_t)g * D + l * E, p.f32, x[y]);
 }
 
 // ---------------------------------------------------------------- page copies
@@ -288,10 +353,10 @@ cudaError_t launch_cache_append(const CacheRowsParams& p, cudaStream_t s) {
 }
 
 cudaError_t launch_cache_read(const CacheRowsParams& p, cudaStream_t s) {
-  const int64_t items = (int64_t)p.c.max_rows * p.c.Hkv;
-  const int per = kRowThreads / 16;
+  const int64_t items = ((int64_t)p.c.max_rows / 2 + 1) * p.c.Hkv;  // pairs that max_rows rows can touch
+  const int per = kReadThreads / 16;
   const dim3 grid(static_cast<unsigned>((items + per - 1) / per), 2, p.c.n_seq);
-  TF_CACHE_DISPATCH(k_cache_read, grid, kRowThreads, s, p);
+  TF_CACHE_DISPATCH(k_cache_read, grid, kReadThreads, s, p);
   return cudaGetLastError();
 }
 
