@@ -15,9 +15,10 @@ namespace tf {
 namespace {
 
 // ---------------------------------------------------------------- rows in and out
-// Half a warp takes one row of one head (D / 16 elements a lane), the two
-// halves of a warp the even and the odd position of a pair: a byte of V's
-// codes holds both positions of a pair, so one warp writes it whole.
+// Append: a lane takes one block of 16 elements of a row (D / 16 lanes a row), so a block's and a row's scale are
+// worked out with few idle repeats: the quantiser's divisions, not memory, bound it (16 x 512 rows of 8 heads,
+// bf16: 27 us with 8 elements a lane).  Even and odd position of a pair sit in one warp: a byte of V's codes holds
+// both, and one lane writes it.
 constexpr int kRowThreads = 128, kReadThreads = 256;
 
 template <int E>
@@ -26,19 +27,21 @@ __device__ __forceinline__ void load_row(const void* base, size_t off, int f32, 
     const float* p = static_cast<const float*>(base) + off;
     if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
 #pragma unroll
-      for (int i = 0; i < E; i += 4) *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(p + i);
+      for (int i = 0; i < E; i += 4) *reinterpret_cast<float4*>(x + i) = __ldg(reinterpret_cast<const float4*>(p + i));
     } else {
 #pragma unroll
       for (int i = 0; i < E; ++i) x[i] = p[i];
     }
   } else {
     const uint16_t* p = static_cast<const uint16_t*>(base) + off;
-    if ((reinterpret_cast<uintptr_t>(p) & (E * 2 - 1)) == 0) {
+    if ((reinterpret_cast<uintptr_t>(p) & (E == 4 ? 7 : 15)) == 0) {
       uint32_t w[E / 2];
-      if constexpr (E == 8)
-        *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
-      else
+      if constexpr (E == 4) {
         *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+      } else {
+#pragma unroll
+        for (int i = 0; i < E / 8; ++i) *reinterpret_cast<uint4*>(w + 4 * i) = *reinterpret_cast<const uint4*>(p + 8 * i);
+      }
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) {
         x[2 * i] = bf16_lo(w[i]);
@@ -81,15 +84,6 @@ __device__ __forceinline__ void store_row(void* base, size_t off, int f32, const
   }
 }
 
-// Largest of a half warp's values; a NaN anywhere gives a NaN.
-__device__ __forceinline__ float half_max_nan(float v, int from, int to) {
-  for (int o = from; o < to; o <<= 1) {
-    const float w = __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    v = (v != v || w != w) ? __int_as_float(0x7FFFFFFF) : fmaxf(v, w);
-  }
-  return v;
-}
-
 // Two floats -> two e2m1 codes in a byte (the first in the low nibble): round to nearest even, +-6 at most.
 __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
   uint16_t d;
@@ -97,29 +91,25 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
   return d;
 }
 
-// x: a lane's E elements of a row.  Quantises them: codes (two per byte), the block's scale byte, the row's scale.
-template <int E>
-__device__ __forceinline__ void quantise_row(const float (&x)[E], uint32_t (&code)[E / 2], uint32_t& sb, float& s) {
-  float am = 0.f;
-  bool bad = false;
+// x: one block of a row, LANES lanes hold the row.  Its codes (two per byte), its scale byte, the row's scale.
+template <int LANES>
+__device__ __forceinline__ void quantise_row(const float (&x)[16], uint32_t (&code)[8], uint32_t& sb, float& s) {
+  uint32_t blk = 0;  // |x| as bits: ordered like the values, infinities and NaN above them
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    am = fmaxf(am, fabsf(x[i]));
-    bad |= !(fabsf(x[i]) < INFINITY);
-  }
-  if (bad) am = __int_as_float(0x7FFFFFFF);
-  const float blk = half_max_nan(am, 1, 16 / E);       // lanes of one block of 16
-  const float row = half_max_nan(blk, 16 / E, 16);     // the half warp
-  s = __fdiv_rn(row, 2688.0f);
+  for (int i = 0; i < 16; ++i) blk = max(blk, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  uint32_t row = blk;
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) row = max(row, __shfl_xor_sync(0xFFFFFFFFu, row, o));
+  s = row >= 0x7F800000u ? __int_as_float(0x7FFFFFFF) : __fdiv_rn(__uint_as_float(row), 2688.0f);
   const float s6 = __fmul_rn(s, 6.0f);
   sb = 0;
   float step = 0.f;
   if (s6 > 0.f) {  // false for NaN
-    sb = __nv_cvt_float_to_fp8(fminf(__fdiv_rn(blk, s6), 448.0f), __NV_SATFINITE, __NV_E4M3);
+    sb = __nv_cvt_float_to_fp8(fminf(__fdiv_rn(__uint_as_float(blk), s6), 448.0f), __NV_SATFINITE, __NV_E4M3);
     step = __fmul_rn(e4m3_value(sb), s);
   }
 #pragma unroll
-  for (int i = 0; i < E / 2; ++i) code[i] = 0;
+  for (int i = 0; i < 8; ++i) code[i] = 0;
   if (!(step > 0.f)) return;
   // The code is that of the rounded quotient x / step.  x * (1 / step) is within 2^-21 of it (two roundings and
   // the reciprocal's); where both ends of that interval have the same code, it is the quotient's (rounding is
@@ -127,7 +117,7 @@ __device__ __forceinline__ void quantise_row(const float (&x)[E], uint32_t (&cod
   const float inv = __fdiv_rn(1.0f, step);
   const bool safe = step > 1e-30f && step < 1e30f;
 #pragma unroll
-  for (int i = 0; i < E / 2; ++i) {
+  for (int i = 0; i < 8; ++i) {
     const float a = x[2 * i] * inv, b = x[2 * i + 1] * inv;
     constexpr float kUp = 1.0f + 4.76837158e-7f, kDown = 1.0f - 4.76837158e-7f;
     const uint32_t c0 = e2m1x2(a * kDown + 0.f, b * kDown + 0.f), c1 = e2m1x2(a * kUp + 0.f, b * kUp + 0.f);
@@ -137,84 +127,71 @@ __device__ __forceinline__ void quantise_row(const float (&x)[E], uint32_t (&cod
   }
 }
 
-// Grid: (position pairs * KV heads, 2 (K, V), sequences); 4 warps a CTA.
+// Grid: (position pairs / 8 (D = 128) or 16, KV heads x (K, V), sequences); 4 warps a CTA.
 template <int D, int FMT>
 __global__ void __launch_bounds__(kRowThreads) k_cache_append(const CacheRowsParams p) {
-  constexpr int E = D / 16;
+  constexpr int LANES = D / 16, PAIRS = 16 / LANES;      // lanes a row, pairs a warp
   using L = Kv4<D>;
   const CacheBatch& c = p.c;
-  const int b = blockIdx.z, isv = blockIdx.y;
-  const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
+  const int b = blockIdx.z, isv = blockIdx.y & 1, g = blockIdx.y >> 1;
+  const int lane = threadIdx.x & 31, l = lane % LANES, half = (lane / LANES) & 1;
   const SeqRows sq = cache_seq(c, b);
-  if (sq.n == 0) return;
   const int p0 = max(sq.len - sq.n, 0);                 // first position written
-  const int item = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-  const int g = item % c.Hkv;
-  const int base = (p0 & ~1) + 2 * (item / c.Hkv);      // the pair's even position
-  if (base >= sq.len) return;
-  const int pos = base + half;
-  const bool mine = pos >= p0 && pos < sq.len;
-  const int page = cache_page(c, b, base / kKvPage);
-  if (page < 0) return;
-  const void* src = isv ? p.v : p.k;
-  float x[E];
+  // the pair's even position; a warp whose first pair is past the end leaves, its other lanes only idle
+  const int base0 = (p0 & ~1) + 2 * PAIRS * (blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5));
+  if (sq.n == 0 || base0 >= sq.len) return;
+  const int base = base0 + 2 * (lane / (2 * LANES)), pos = base + half;
+  const int page = base < sq.len ? cache_page(c, b, base / kKvPage) : -1;
+  const bool mine = page >= 0 && pos >= p0 && pos < sq.len;
+  float x[16];
 #pragma unroll
-  for (int i = 0; i < E; ++i) x[i] = 0.f;
+  for (int i = 0; i < 16; ++i) x[i] = 0.f;
   if (mine)
-    load_row<E>(src, (size_t)(sq.r0 + pos - (sq.len - sq.n)) * p.stride + (size_t)g * D + l * E, p.f32, x);
+    load_row<16>(isv ? p.v : p.k, (size_t)(sq.r0 + pos - (sq.len - sq.n)) * p.stride + (size_t)g * D + l * 16, p.f32, x);
   const int r = pos % kKvPage;
-  uint8_t* pool = const_cast<uint8_t*>(isv ? c.V : c.K);
+  uint8_t* head = const_cast<uint8_t*>(isv ? c.V : c.K) +
+                  ((size_t)max(page, 0) * c.Hkv + g) * (FMT ? L::kBytes : kKvPage * D * 2);
   if constexpr (FMT == 0) {
-    uint16_t* dst = reinterpret_cast<uint16_t*>(pool) + (((size_t)page * c.Hkv + g) * kKvPage + r) * D + l * E;
     if (mine) {
-      uint32_t w[E / 2];
+      uint32_t w[8];
 #pragma unroll
-      for (int i = 0; i < E / 2; ++i)
+      for (int i = 0; i < 8; ++i)
         w[i] = static_cast<uint32_t>(f32_to_bf16(x[2 * i])) | static_cast<uint32_t>(f32_to_bf16(x[2 * i + 1])) << 16;
-      if constexpr (E == 8)
-        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-      else
-        *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+      uint4* dst = reinterpret_cast<uint4*>(head + (r * D + l * 16) * 2);
+      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
   } else {
-    uint8_t* head = pool + ((size_t)page * c.Hkv + g) * L::kBytes;
-    uint32_t code[E / 2], sb;
+    uint32_t code[8], sb;
     float s;
-    quantise_row<E>(x, code, sb, s);
-    if (mine && l == 0) reinterpret_cast<float*>(head + L::kRows)[r] = s;
-    const int blk = l * E / 16;
-    if (mine && (l * E) % 16 == 0)
-      head[L::kCodes + (isv ? blk * kKvPage + r : r * (D / 16) + blk)] = static_cast<uint8_t>(sb);
+    quantise_row<LANES>(x, code, sb, s);
+    if (mine) {
+      if (l == 0) reinterpret_cast<float*>(head + L::kRows)[r] = s;
+      head[L::kCodes + (isv ? l * kKvPage + r : r * (D / 16) + l)] = static_cast<uint8_t>(sb);
+    }
     if (!isv) {
-      uint32_t w = 0;
-#pragma unroll
-      for (int i = 0; i < E / 2; ++i) w |= code[i] << (8 * i);
-      if (mine) {
-        if constexpr (E == 8)
-          *reinterpret_cast<uint32_t*>(head + r * (D / 2) + l * 4) = w;
-        else
-          *reinterpret_cast<uint16_t*>(head + r * (D / 2) + l * 2) = static_cast<uint16_t>(w);
-      }
+      if (mine)
+        *reinterpret_cast<uint2*>(head + r * (D / 2) + l * 8) =
+            make_uint2(code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24,
+                       code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24);
     } else {
       // the even position's lane writes the pair's bytes; a position that this
       // call does not write keeps its nibble
-      uint32_t* dst = reinterpret_cast<uint32_t*>(head + L::v_byte(base % kKvPage, l * E));
-      const bool both = __shfl_xor_sync(0xFFFFFFFFu, mine ? 1 : 0, 16) && mine;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(head + L::v_byte(base % kKvPage, l * 16));
+      const bool both = __shfl_xor_sync(0xFFFFFFFFu, mine ? 1 : 0, LANES) && mine;
+      uint32_t out[4];
 #pragma unroll
-      for (int w = 0; w < E / 4; ++w) {
-        uint32_t v = 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t two = code[2 * w + i];
-          v |= ((two & 15u) | (two >> 4) << 8) << (16 * i);
-        }
-        const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t two = code[2 * w] | code[2 * w + 1] << 16;      // elements 0, 1 and 2, 3: a nibble each
+        out[w] = (two & 0x000F000Fu) | (two & 0x00F000F0u) << 4;       // ... a byte each
+        const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, out[w], LANES);
         if (both) {
-          if (half == 0) dst[w] = v | (o << 4);
+          out[w] |= o << 4;
         } else if (mine) {
-          dst[w] = half ? (dst[w] & 0x0F0F0F0Fu) | (v << 4) : (dst[w] & 0xF0F0F0F0u) | v;
+          out[w] = half ? (dst[w] & 0x0F0F0F0Fu) | (out[w] << 4) : (dst[w] & 0xF0F0F0F0u) | out[w];
         }
       }
+      if (both ? half == 0 : mine) *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
     }
   }
 }
@@ -345,9 +322,9 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache_copy(const __grid_consta
   } while (0)
 
 cudaError_t launch_cache_append(const CacheRowsParams& p, cudaStream_t s) {
-  const int64_t items = ((int64_t)p.c.max_rows / 2 + 1) * p.c.Hkv;  // pairs that max_rows rows can touch
-  const int per = kRowThreads / 32;
-  const dim3 grid(static_cast<unsigned>((items + per - 1) / per), 2, p.c.n_seq);
+  const int64_t pairs = (int64_t)p.c.max_rows / 2 + 1;  // that max_rows rows can touch
+  const int per = (kRowThreads / 32) * (256 / p.c.D);
+  const dim3 grid(static_cast<unsigned>((pairs + per - 1) / per), 2 * p.c.Hkv, p.c.n_seq);
   TF_CACHE_DISPATCH(k_cache_append, grid, kRowThreads, s, p);
   return cudaGetLastError();
 }

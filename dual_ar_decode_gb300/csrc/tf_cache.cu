@@ -18,7 +18,7 @@ bool batch_of(const tf_kv_cache* c, CacheBatch* b) {
   if (!c || !c->K || !c->V || !c->block_table || !c->lengths) return false;
   if (c->format != TF_KV_BF16 && c->format != TF_KV_NVFP4) return false;
   if (c->head_dim != 64 && c->head_dim != 128) return false;
-  if (c->n_kv_heads < 1 || c->n_kv_heads > 65535 || c->n_pages < 1 || c->table_stride < 1 || c->n_seq < 1 ||
+  if (c->n_kv_heads < 1 || c->n_kv_heads > 32767 || c->n_pages < 1 || c->table_stride < 1 || c->n_seq < 1 ||
       c->n_seq > 65535 || c->n_rows < 0 || c->max_rows < 0 || c->max_length < 0)
     return false;
   if ((int64_t)c->n_pages * c->n_kv_heads * kKvPage >= (1ll << 31)) return false;
