@@ -1,6 +1,7 @@
 """ctypes binding of the C ABI in include/tf.h (argument marshalling only)."""
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -383,10 +384,11 @@ def op_cache_read(cache, k_dev, v_dev, dtype, stream=0, stride=0):
 
 def op_cache_copy(pools, page_bytes, n_pages, src, dst, stream=0):
     """Copies pages src[i] -> dst[i] (host ids) in every pool (device pointers)."""
-    bases = (ctypes.c_void_p * len(pools))(*pools)
+    bases = array.array("Q", pools)
     src = np.ascontiguousarray(src, dtype=np.int32)
     dst = np.ascontiguousarray(dst, dtype=np.int32)
     if src.shape != dst.shape or src.ndim != 1:
         raise ValueError("src and dst are lists of the same length")
-    _check(lib().tf_op_cache_copy(bases, len(pools), page_bytes, n_pages, src.ctypes.data, dst.ctypes.data,
+    _check(lib().tf_op_cache_copy(bases.buffer_info()[0], len(bases), page_bytes, n_pages,
+                                  src.__array_interface__["data"][0], dst.__array_interface__["data"][0],
                                   src.size, stream))

@@ -566,21 +566,33 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + x * 128 + lanes, t_o = tmem + 256 + x * 128 + lanes;
     const int col0 = x * 128 + (warp & 3) * 32;   // the warp's first pair
-    // Q (by these 256 threads): pair m of the CTA is row (c0 + m) / G, head (c0 + m) % G; rows past the last pair are zero.
-    for (int e = threadIdx.x; e < 256 * (D / 8); e += 256) {
-      const int m = e / (D / 8), ch = e % (D / 8), cc = c0 + m;
-      uint4* dst = chunk_at(smem + (m >> 7) * C::kTile, m & 127, ch);
-      const uint16_t* src = static_cast<const uint16_t*>(p.q) + (size_t)(sq.r0 + cc / G) * p.q_stride +
-                            (size_t)(hkv * G + cc % G) * D + ch * 8;
-      if (m >= ncol) {
-        *dst = make_uint4(0u, 0u, 0u, 0u);
-      } else if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-      } else {
-        uint32_t w[4];
+    // Q (by these 256 threads): pair m of the CTA is row (c0 + m) / G, head (c0 + m) % G; rows past the last pair
+    // are zero.  A warp copies kLines pairs at a time; lane i works out where the i-th of its 32 pairs lies.
+    constexpr int kChunks = D / 8, kLines = 32 / kChunks;
+    auto pair_at = [&](int m, int64_t stride) {  // element offset of a pair's row
+      const int cc = c0 + m;
+      return (int64_t)(sq.r0 + cc / G) * stride + (int64_t)(hkv * G + cc % G) * D;
+    };
+    auto from_lane = [&](int64_t v, int src) {
+      return static_cast<int64_t>(__shfl_sync(0xFFFFFFFFu, static_cast<long long>(v), src));
+    };
+    {
+      const int64_t at = pair_at(lane / kLines * (8 * kLines) + warp * kLines + lane % kLines, p.q_stride);
+#pragma unroll 4
+      for (int it = 0; it < kChunks; ++it) {
+        const int m = it * (8 * kLines) + warp * kLines + lane / kChunks, ch = lane % kChunks;
+        uint4* dst = chunk_at(smem + (m >> 7) * C::kTile, m & 127, ch);
+        const uint16_t* src = static_cast<const uint16_t*>(p.q) + from_lane(at, it * kLines + lane / kChunks) + ch * 8;
+        if (m >= ncol) {
+          *dst = make_uint4(0u, 0u, 0u, 0u);
+        } else if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+        } else {
+          uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = src[2 * i] | static_cast<uint32_t>(src[2 * i + 1]) << 16;
-        *dst = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int i = 0; i < 4; ++i) w[i] = src[2 * i] | static_cast<uint32_t>(src[2 * i + 1]) << 16;
+          *dst = make_uint4(w[0], w[1], w[2], w[3]);
+        }
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -692,7 +704,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) mx[k] = -INFINITY;
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 3; q >= 0; --q) {
             uint32_t s[2][16], see[4];
             tm_frag_ld(t_s + q * 32, s[0]);
             tm_frag_ld(t_s + (16u << 16) + q * 32, s[1]);
@@ -708,6 +720,13 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
                 if ((see[k] >> (8 * i)) & 1u) mx[k] = fmaxf(mx[k], __uint_as_float(sr[0]) * ks.x);
                 if ((see[k] >> (8 * i)) & 2u) mx[k] = fmaxf(mx[k], __uint_as_float(sr[1]) * ks.y);
               }
+            }
+            // to begin with any reference near the maximum does: the keys of one quarter, if every row sees some
+            if (round == 0) {
+              bool none = false;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) none |= mx[k] == -INFINITY;
+              if (!__any_sync(0xFFFFFFFFu, none)) break;
             }
           }
           float alpha[4];
@@ -795,13 +814,13 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
         }
       }
       __syncwarp();
+      const int64_t at = pair_at(col0 + lane, p.out_stride);
 #pragma unroll 4
-      for (int e = lane; e < 32 * (D / 8); e += 32) {
-        const int r = e / (D / 8), ch = e % (D / 8), col = col0 + r, cc = c0 + col;
+      for (int it = 0; it < kChunks; ++it) {
+        const int r = it * kLines + lane / kChunks, ch = lane % kChunks;
         const uint4 v = *chunk_at(mine, r0 + r, ch);
-        if (col < ncol) {
-          uint16_t* dst = static_cast<uint16_t*>(p.out) + (size_t)(sq.r0 + cc / G) * p.out_stride +
-                          (size_t)(hkv * G + cc % G) * D + ch * 8;
+        uint16_t* dst = static_cast<uint16_t*>(p.out) + from_lane(at, r) + ch * 8;
+        if (col0 + r < ncol) {
           if ((reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
             *reinterpret_cast<uint4*>(dst) = v;
           } else {
