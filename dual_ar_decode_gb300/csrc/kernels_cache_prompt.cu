@@ -190,10 +190,14 @@ __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t v) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(v)));
   return h;
 }
+// The products of two f16 pairs as floats (mixed-precision FMA: conversion and product in one).
 __device__ __forceinline__ float2 scaled(uint32_t v, uint32_t s) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(s));
-  return __half22float2(*reinterpret_cast<const __half2*>(&d));
+  float2 d;
+  asm("{.reg .b16 vl, vh, sl, sh; mov.b32 {vl, vh}, %2; mov.b32 {sl, sh}, %3;"
+      " fma.rn.f32.f16 %0, vl, sl, %4; fma.rn.f32.f16 %1, vh, sh, %4;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "r"(v), "r"(s), "f"(0.f));
+  return d;
 }
 // Two floats in one 64-bit operand of the packed float32 instructions.
 __device__ __forceinline__ uint64_t pair2(float a, float b) {
@@ -305,10 +309,10 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *tmem_slot;
 
-  // FMT 1: the softmax's warpgroups take registers from the other two: 256 x 168 + 256 x 88 = the launch's
+  // FMT 1: the softmax's warpgroups take registers from the other two: 256 x 160 + 256 x 96 = the launch's
   // 512 x 128
   if (warp >= 8) {
-  if constexpr (FMT == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if constexpr (FMT == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
   if (warp == C::kMmaWarp) {
     // ---------------------------------------------------------------- MMA issuer
     if (lane == 0) {
@@ -502,8 +506,11 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
           const int e = i * 32 + lane, r = w * 32 + e / PR, q = e % PR;
-          const uint32_t words[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-          const uint32_t s2 = e4m3x2_f16(ksb[i]);
+          // (the lanes of the row's upper half store their blocks the other way round: no bank conflicts)
+          const bool swap = (q >> 1) & 1;
+          const uint32_t words[4] = {swap ? raw[i].z : raw[i].x, swap ? raw[i].w : raw[i].y,
+                                     swap ? raw[i].x : raw[i].z, swap ? raw[i].y : raw[i].w};
+          const uint32_t s2 = e4m3x2_f16(swap ? __byte_perm(ksb[i], 0, 0x4401) : ksb[i]);
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             uint32_t h[4], o[4];
@@ -514,7 +521,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
               const float2 f = scaled(h[y], sd);
               o[y] = pack_bf16(f.x, f.y);
             }
-            *chunk_at(kt, r, 4 * q + x) = make_uint4(o[0], o[1], o[2], o[3]);
+            *chunk_at(kt, r, 4 * q + (x ^ (swap ? 2 : 0))) = make_uint4(o[0], o[1], o[2], o[3]);
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -528,7 +535,9 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
           const int v = v_unit(i), r = v_row(v), blk = (v % (D / 4)) / 4, row = w * 32 + r;
-          const uint32_t words[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+          const bool swap = blk & 1;
+          const uint32_t words[4] = {swap ? raw[i].z : raw[i].x, swap ? raw[i].w : raw[i].y,
+                                     swap ? raw[i].x : raw[i].z, swap ? raw[i].y : raw[i].w};
           uint32_t sb = vsb[i];
           if ((dead >> r) & 1u) sb &= 0xFF00u;
           if ((dead >> r) & 2u) sb &= 0x00FFu;
@@ -547,8 +556,8 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
               o0[2 + y] = pack_bf16(g0.x, g1.x);
               o1[2 + y] = pack_bf16(g0.y, g1.y);
             }
-            *chunk_at(vt, row, 2 * blk + x / 2) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-            *chunk_at(vt, row + 1, 2 * blk + x / 2) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+            *chunk_at(vt, row, 2 * blk + (x / 2 ^ (swap ? 1 : 0))) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+            *chunk_at(vt, row + 1, 2 * blk + (x / 2 ^ (swap ? 1 : 0))) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -559,7 +568,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
     }
   }
   } else {
-    if constexpr (FMT == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    if constexpr (FMT == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     // ---------------------------------------------------------------- softmax: a warp has 32 pairs (its TMEM
     // lanes); lane (g, t) holds pairs g, g + 8, g + 16, g + 24 and columns 2 t, 2 t + 1 of every 8
     const int x = warp >> 2, lg = lane >> 2, lt = lane & 3;
