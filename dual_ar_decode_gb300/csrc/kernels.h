@@ -382,6 +382,9 @@ inline int64_t cache_head_bytes(int fmt, int D) {
 cudaError_t launch_cache_decode(const CacheAttnParams& p, cudaStream_t s);
 // Many rows per sequence, bfloat16 rows only (any number is right).
 cudaError_t launch_cache_prompt(const CacheAttnParams& p, cudaStream_t s);
+// What either takes, roughly, in microseconds.
+float cache_decode_us(const CacheAttnParams& p);
+float cache_prompt_us(const CacheAttnParams& p);
 cudaError_t launch_cache_append(const CacheRowsParams& p, cudaStream_t s);
 cudaError_t launch_cache_read(const CacheRowsParams& p, cudaStream_t s);
 // n copies of 16-byte words: page src[i] -> page dst[i] of every pool.

@@ -866,6 +866,38 @@ __global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
   }
 }
 
+// How a launch is cut.
+struct DecPlan {
+  int64_t groups;  // (sequence, KV head, tile of columns): an upper bound, rows are n_rows at most in all
+  int64_t units;   // stages of the longest group
+  int cs;          // CTAs per group
+};
+// Columns of a tile, in eights.  bf16 pages: as many as fit the registers share a read (16 sequences x 5 rows x 4
+// heads: 27 us with 24 columns, 32 with 8).  4-bit pages: 8; more would leave one CTA an SM, and the products'
+// latency shows (22 us with 8, 28 with 24).
+int decode_nt(const CacheAttnParams& p) {
+  const int64_t cols = (int64_t)p.c.max_rows * (p.Hq / p.c.Hkv);
+  return p.c.fmt || cols <= 8 ? 1 : cols <= 16 ? 2 : 3;
+}
+DecPlan decode_plan(const CacheAttnParams& p, int nt, int keys_per_stage) {
+  const int64_t G = p.Hq / p.c.Hkv, cols = 8 * nt;
+  const int64_t keys = p.window > 0 ? std::min<int64_t>(p.c.max_len, (int64_t)p.window + p.sinks + 8) : p.c.max_len;
+  DecPlan d;
+  d.groups = std::min(((int64_t)p.c.max_rows * G + cols - 1) / cols * p.c.n_seq, p.c.n_rows * G / cols + p.c.n_seq) *
+             p.c.Hkv;
+  d.units = (keys + keys_per_stage - 1) / keys_per_stage;
+  // Enough CTAs to fill the SMs (4-bit: two each), as long as a warp still gets a stage (measured: one more doubling
+  // costs 5-30%, one less leaves SMs idle).  16, beyond the portable cluster size, starts slowly and pays only for
+  // one long sequence (131072 positions, 8 KV heads: 101 -> 79 us; 4096 positions: 8.9 -> 11 us).
+  const int slots = (p.c.fmt ? 2 : 1) * 152;
+  d.cs = 1;
+  // (bf16: one CTA an SM, so a doubling that starts a second wave gains nothing)
+  auto more = [&](int64_t ctas) { return p.c.fmt ? ctas < slots : ctas * 2 < slots || ctas * 20 < slots * 11; };
+  while (d.cs < 8 && more(d.groups * d.cs) && (int64_t)d.cs * 8 < d.units) d.cs *= 2;
+  if (d.cs == 8 && d.groups * 8 < 152 && d.units >= 1024) d.cs = 16;
+  return d;
+}
+
 template <int D, int FMT, int NT, int F32>
 cudaError_t launch_decode_t(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnParams& p,
                             cudaStream_t s) {
@@ -878,21 +910,11 @@ cudaError_t launch_decode_t(const CUtensorMap& mk, const CUtensorMap& mv, const 
     return cudaFuncSetAttribute(k_cache_decode<D, FMT, NT, F32>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   });
   if (e) return e;
-  const int G = p.Hq / p.c.Hkv;
-  const int64_t tiles = ((int64_t)p.c.max_rows * G + C::kCols - 1) / C::kCols;
-  // CTAs per group: enough to fill the SMs (4-bit: two CTAs each), as long as a warp still gets a stage
-  // (measured: one more doubling costs 5-30%, one less leaves SMs idle).  16, beyond the portable
-  // cluster size, starts slowly and pays only for one long sequence (131072 positions, 8 KV heads: 101 ->
-  // 79 us; 4096 positions: 8.9 -> 11 us).
-  const int64_t keys = p.window > 0 ? std::min<int64_t>(p.c.max_len, (int64_t)p.window + p.sinks + 8) : p.c.max_len;
-  const int64_t groups = tiles * p.c.Hkv * p.c.n_seq;
-  const int64_t units = (keys + C::kKeys - 1) / C::kKeys;
-  const int slots = (FMT ? 2 : 1) * 152;
-  int cs = 1;
-  while (cs < 8 && groups * cs < slots && (int64_t)cs * C::kWarps < units) cs *= 2;
-  if (cs == 8 && groups * 8 < 152 && units >= 1024) cs = 16;
+  const DecPlan d = decode_plan(p, NT, C::kKeys);
+  const int64_t tiles = ((int64_t)p.c.max_rows * (p.Hq / p.c.Hkv) + C::kCols - 1) / C::kCols;
+  const int cs = d.cs;
   if (tiles * cs > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  const int sorted = p.c.n_seq > 1 && p.c.n_seq <= kSortMax && groups * cs > 152 ? 1 : 0;
+  const int sorted = p.c.n_seq > 1 && p.c.n_seq <= kSortMax && d.groups * cs > 152 ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * cs), p.c.Hkv, p.c.n_seq);
   cfg.blockDim = dim3(256);
@@ -911,18 +933,24 @@ cudaError_t launch_decode_t(const CUtensorMap& mk, const CUtensorMap& mv, const 
 template <int D, int FMT, int F32>
 cudaError_t launch_decode_n(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnParams& p,
                             cudaStream_t s) {
-  // Columns of a tile.  bf16 pages: as many as fit the registers share a read (16 sequences x 5 rows x 4
-  // heads: 27 us with 24 columns, 32 with 8).  4-bit pages: 8; more would leave one CTA an SM, and the
-  // products' latency shows (22 us with 8, 28 with 24).
-  const int64_t cols = (int64_t)p.c.max_rows * (p.Hq / p.c.Hkv);
+  const int nt = decode_nt(p);
   if constexpr (FMT == 0) {
-    if (cols > 16) return launch_decode_t<D, FMT, 3, F32>(mk, mv, p, s);
-    if (cols > 8) return launch_decode_t<D, FMT, 2, F32>(mk, mv, p, s);
+    if (nt == 3) return launch_decode_t<D, FMT, 3, F32>(mk, mv, p, s);
+    if (nt == 2) return launch_decode_t<D, FMT, 2, F32>(mk, mv, p, s);
   }
   return launch_decode_t<D, FMT, 1, F32>(mk, mv, p, s);
 }
 
 }  // namespace
+
+// Measured as cache_prompt_us: start and end of a CTA, and a stage of a warp (the SM full).
+float cache_decode_us(const CacheAttnParams& p) {
+  const DecPlan d = decode_plan(p, decode_nt(p), p.c.fmt ? kKvPage : kKvPage / 2);
+  const int slots = (p.c.fmt ? 2 : 1) * 152;
+  const int64_t waves = (d.groups * d.cs + slots - 1) / slots;
+  const float stage = p.c.fmt ? (p.c.D == 128 ? 2.05f : 1.15f) : (p.c.D == 128 ? 1.3f : 1.05f);
+  return static_cast<float>(waves) * ((p.c.fmt ? 6.f : 5.f) + stage * static_cast<float>((d.units + 8 * d.cs - 1) / (8 * d.cs)));
+}
 
 cudaError_t launch_cache_decode(const CacheAttnParams& p, cudaStream_t s) {
   CUtensorMap mk = {}, mv = {};

@@ -234,10 +234,11 @@ __device__ __forceinline__ uint32_t sees(int base, int pos, int low, int sinks) 
   return ones(pos - base + 1) & (~ones(low - base) | ones(sinks - base));
 }
 
-template <int D, int FMT>
+template <int D, int FMT, int NX>
 __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
     k_cache_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                    const CacheAttnParams p) {
+  constexpr int span = 128 * NX;  // pairs of the CTA: NX tiles
   using C = PromptCfg<D, FMT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
   const int G = p.Hq / c.Hkv;
   const SeqRows sq = cache_seq(c, b);
   const int tile = static_cast<int>(gridDim.x - 1 - blockIdx.x);  // the last rows, which see most, first
-  const int c0 = tile * 256, ncol = min(256, sq.n * G - c0);
+  const int c0 = tile * span, ncol = min(span, sq.n * G - c0);
   if (ncol <= 0) return;
   const int first = sq.len - sq.n;
   const int posmin = first + c0 / G, posmax = first + (c0 + ncol - 1) / G;
@@ -331,13 +332,13 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         if (ok) {
           score(0, 0);
-          score(1, 0);
+          if constexpr (NX > 1) score(1, 0);
           mma_commit(&k_empty[0]);
         }
       }
       for (int j = 0; ok && j < nt; ++j) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < NX; ++x) {
           ok = ok && bar_wait(&p_full[x], j & 1) && (x || bar_wait(FMT ? &v_full[j & 1] : &v_clean[j & 1], (j >> 1) & 1));
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -346,7 +347,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
           for (int kk = 0; kk < 8; ++kk)
             mma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, desc_mn(vb + kk * 2048), C::kIdescO,
                    (j > 0 || kk > 0) ? 1u : 0u);
-          if (x) mma_commit(&v_empty[j & 1]);
+          if (x == NX - 1) mma_commit(&v_empty[j & 1]);
           if (j + 1 < nt) {
             if (!x) {
               ok = bar_wait(&k_full[(j + 1) & 1], ((j + 1) >> 1) & 1);
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
               asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             }
             score(x, j + 1);  // after the product that reads P_x, in issue order; its commit covers both
-            if (x) mma_commit(&k_empty[(j + 1) & 1]);
+            if (x == NX - 1) mma_commit(&k_empty[(j + 1) & 1]);
           } else {
             mma_commit(&o_done[x]);
           }
@@ -618,7 +619,8 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
       l[k] = 0.f;
     }
     bool ok = true;
-    for (int j = 0; j < nt; ++j) {
+    const int mine = x < NX ? nt : 0;
+    for (int j = 0; j < mine; ++j) {
       if (!(ok = bar_wait_warp(&s_full[x], j & 1))) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const Info* in = info(j);
@@ -786,8 +788,8 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       mbar_arrive(&p_full[x]);
     }
-    if (ok && nt > 0) ok = bar_wait_warp(&o_done[x], 0);
-    if (ok) {
+    if (ok && mine > 0) ok = bar_wait_warp(&o_done[x], 0);
+    if (ok && x < NX) {
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       // the sums of this lane's own row (pair `lane` of the warp), whose outputs it stores
       float total = 0.f;
@@ -802,7 +804,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
       const float inv = total == 0.f ? 0.f : 1.f / total;
       // Rows go out through the warp's 32 rows of the Q tile (every product that read it is done), so that a
       // store covers whole rows.
-      uint8_t* mine = smem + x * C::kTile;
+      uint8_t* rows = smem + x * C::kTile;
       const int r0 = (warp & 3) * 32;
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {
@@ -819,7 +821,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
 #pragma unroll
           for (int h = 0; h < 4; ++h)
             w[h] = total == 0.f ? 0u : pack_bf16(t[i + 2 * h] * inv, t[i + 2 * h + 1] * inv);
-          *chunk_at(mine, r0 + lane, (d + i) / 8) = make_uint4(w[0], w[1], w[2], w[3]);
+          *chunk_at(rows, r0 + lane, (d + i) / 8) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
       __syncwarp();
@@ -827,7 +829,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
 #pragma unroll 4
       for (int it = 0; it < kChunks; ++it) {
         const int r = it * kLines + lane / kChunks, ch = lane % kChunks;
-        const uint4 v = *chunk_at(mine, r0 + r, ch);
+        const uint4 v = *chunk_at(rows, r0 + r, ch);
         uint16_t* dst = static_cast<uint16_t*>(p.out) + from_lane(at, r) + ch * 8;
         if (col0 + r < ncol) {
           if ((reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
@@ -842,7 +844,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
           }
         }
       }
-    } else if (lane == 0) {
+    } else if (!ok && lane == 0) {
       *failed = 1;
     }
   }
@@ -855,22 +857,52 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
   }
 }
 
-template <int D, int FMT>
-cudaError_t launch_prompt_t(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnParams& p,
+// CTAs of a launch with `span` pairs each (an upper bound: rows are n_rows at most in all).
+int64_t prompt_ctas(const CacheAttnParams& p, int span) {
+  const int64_t G = p.Hq / p.c.Hkv;
+  const int64_t each = ((int64_t)p.c.max_rows * G + span - 1) / span * p.c.n_seq;
+  return std::min(each, p.c.n_rows * G / span + p.c.n_seq) * p.c.Hkv;
+}
+// Pairs of a CTA: 128 while that still is one wave of CTAs (a tile of keys takes 1.48 us with one 128-pair tile and
+// 1.63 with two, bf16, D = 128, so two pay once the CTAs queue).
+int prompt_span(const CacheAttnParams& p) { return prompt_ctas(p, 128) <= 152 ? 128 : 256; }
+
+template <int D, int FMT, int NX>
+cudaError_t launch_prompt_x(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnParams& p,
                             cudaStream_t s) {
   using C = PromptCfg<D, FMT>;
   static DeviceOnce once;
   cudaError_t e = device_once(once, [] {
-    return cudaFuncSetAttribute(k_cache_prompt<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    return cudaFuncSetAttribute(k_cache_prompt<D, FMT, NX>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   });
   if (e) return e;
-  const int64_t tiles = ((int64_t)p.c.max_rows * (p.Hq / p.c.Hkv) + 255) / 256;
+  constexpr int span = 128 * NX;
+  const int64_t tiles = ((int64_t)p.c.max_rows * (p.Hq / p.c.Hkv) + span - 1) / span;
   if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  k_cache_prompt<D, FMT><<<dim3(static_cast<unsigned>(tiles), p.c.Hkv, p.c.n_seq), C::kThreads, C::kSmem, s>>>(mk, mv, p);
+  k_cache_prompt<D, FMT, NX><<<dim3(static_cast<unsigned>(tiles), p.c.Hkv, p.c.n_seq), C::kThreads, C::kSmem, s>>>(
+      mk, mv, p);
   return cudaGetLastError();
 }
 
+template <int D, int FMT>
+cudaError_t launch_prompt_t(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnParams& p,
+                            cudaStream_t s) {
+  return prompt_span(p) == 128 ? launch_prompt_x<D, FMT, 1>(mk, mv, p, s) : launch_prompt_x<D, FMT, 2>(mk, mv, p, s);
+}
+
 }  // namespace
+
+// Measured with rows that see everything (4-bit and bf16 pages, D = 64 and 128, 1 and 8 sequences, 512 and 4096
+// positions): start and end of a CTA, and a tile of 128 keys.
+float cache_prompt_us(const CacheAttnParams& p) {
+  const int span = prompt_span(p);
+  const int64_t waves = (prompt_ctas(p, span) + 151) / 152;
+  const int64_t rows = std::max<int64_t>(1, span / (p.Hq / p.c.Hkv));
+  const int64_t keys = p.window > 0 ? std::min<int64_t>(p.c.max_len, (int64_t)p.window + p.sinks + rows + 64) : p.c.max_len;
+  const float start = p.c.fmt ? (p.c.D == 128 ? 8.5f : 7.0f) : (p.c.D == 128 ? 7.5f : 6.3f);
+  const float tile = (p.c.fmt ? (p.c.D == 128 ? 2.3f : 2.0f) : (p.c.D == 128 ? 1.63f : 1.43f)) * (span == 128 ? 0.91f : 1.f);
+  return static_cast<float>(waves) * (start + tile * static_cast<float>((keys + 127) / 128));
+}
 
 cudaError_t launch_cache_prompt(const CacheAttnParams& p, cudaStream_t s) {
   if (p.f32) return cudaErrorInvalidValue;

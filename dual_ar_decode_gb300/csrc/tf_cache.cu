@@ -10,8 +10,6 @@ namespace {
 
 using namespace tf;
 
-constexpr int64_t kPromptPairs = 64;
-
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 bool batch_of(const tf_kv_cache* c, CacheBatch* b) {
@@ -96,8 +94,8 @@ tf_status tf_op_attention_cache(const tf_kv_cache* cache, const void* q, int64_t
   p.sinks = sinks < (1 << 30) ? sinks : 1 << 30;
   const double sc = scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)p.c.D);
   p.scale_log2 = static_cast<float>(sc * 1.4426950408889634);
-  // bfloat16 rows that fill a good part of a 256-pair tile go to the tensor-core kernel
-  const bool many = !p.f32 && (int64_t)p.c.max_rows * (n_heads / p.c.Hkv) >= kPromptPairs;
+  // bfloat16 rows take the tensor-core kernel where it is the faster one by what both were measured at
+  const bool many = !p.f32 && cache_prompt_us(p) < cache_decode_us(p);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return (many ? launch_cache_prompt(p, s) : launch_cache_decode(p, s)) == cudaSuccess ? TF_OK : TF_E_CUDA;
 }
