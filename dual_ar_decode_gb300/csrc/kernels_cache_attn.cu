@@ -166,9 +166,11 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t (&part)[NP
 }
 
 // Shared memory and shape of one instantiation.
-template <int D, int FMT, int NT, int F32>
+template <int D, int FMT, int NT, int F32, int W>
 struct DecCfg {
-  static constexpr int kWarps = 8;
+  static constexpr int kWarps = W;
+  static constexpr int kThreads = 32 * W;
+  static constexpr int kPerSm = FMT ? 16 / W : 8 / W;      // CTAs an SM (registers and shared memory allow them)
   static constexpr int kKeys = FMT ? 32 : 16;               // positions of a stage (a page, or half a page)
   static constexpr int kHalf = FMT ? Kv4<D>::kBytes : 16 * D * 2;  // K (or V) bytes of a stage
   static constexpr int kStage = 2 * kHalf;
@@ -198,11 +200,11 @@ struct TileRows {
   int c0, nc;         // the tile's first column and how many it has
 };
 
-template <int D, int FMT, int NT, int F32>
-__global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
+template <int D, int FMT, int NT, int F32, int W>
+__global__ void __launch_bounds__(32 * W, DecCfg<D, FMT, NT, F32, W>::kPerSm)
     k_cache_decode(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                    const CacheAttnParams p, const int csize, const int sorted) {
-  using C = DecCfg<D, FMT, NT, F32>;
+  using C = DecCfg<D, FMT, NT, F32, W>;
   constexpr int KB = C::kKeys / 8;   // blocks of 8 keys in a stage
   constexpr int MT = D / 16;         // 16-row tiles of the head dimension
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -218,12 +220,12 @@ __global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
   int b = blockIdx.z;
   if (sorted) {
     __shared__ int lens[kSortMax], chosen;
-    const int t = threadIdx.x, n = c.n_seq;
-    const int mine = t < n ? __ldg(c.len + t) : 0;
-    if (t < n) lens[t] = mine;
+    const int n = c.n_seq;
+    for (int t = threadIdx.x; t < n; t += C::kThreads) lens[t] = __ldg(c.len + t);
     __syncthreads();
-    if (t < n) {
+    for (int t = threadIdx.x; t < n; t += C::kThreads) {
       int r = 0;
+      const int mine = lens[t];
       for (int i = 0; i < n; ++i) r += (lens[i] > mine || (lens[i] == mine && i < t)) ? 1 : 0;
       if (r == b) chosen = t;
     }
@@ -265,10 +267,11 @@ __global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
   __syncwarp();
 
   // the queries' loads go out first: they are used after the stages have been asked for
-  float xq[NT][D / 32];  // columns warp, warp + 8, ...; dims lane, lane + 32, ...
+  constexpr int QC = C::kCols / C::kWarps;  // columns a warp prepares: warp, warp + kWarps, ...
+  float xq[QC][D / 32];                     // dims lane, lane + 32, ...
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int col = n * 8 + warp, cc = c0 + col, row = cc / G, h = hkv * G + cc % G;
+  for (int n = 0; n < QC; ++n) {
+    const int col = n * C::kWarps + warp, cc = c0 + col, row = cc / G, h = hkv * G + cc % G;
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) {
       xq[n][e] = 0.f;
@@ -322,8 +325,8 @@ __global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
   // ---- queries: the parts of every column in the order the products read them.  A column's queries are
   // scaled by a power of two so that the largest is in [2^14, 2^15) (FMT 1: f16 holds them).
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int col = n * 8 + warp;
+  for (int n = 0; n < QC; ++n) {
+    const int col = n * C::kWarps + warp;
     const float(&x)[D / 32] = xq[n];
     float up = 1.f;
     if constexpr (FMT == 1) {
@@ -775,7 +778,7 @@ __global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
   };
   if (csize > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   // The CTA's maximum and sum of every column, to every rank.
-  for (int e = threadIdx.x; e < csize * C::kCols; e += 256) {
+  for (int e = threadIdx.x; e < csize * C::kCols; e += C::kThreads) {
     const int col = e % C::kCols, r = e / C::kCols;
     float M = -INFINITY, L = 0.f;
 #pragma unroll
@@ -790,7 +793,7 @@ __global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
   }
   // The CTA's outputs, 4 dims of a column each, to the rank that finishes them.
   const int quads = ncol * (D / 4), share = (quads + csize - 1) / csize;
-  for (int e = threadIdx.x; e < quads; e += 256) {
+  for (int e = threadIdx.x; e < quads; e += C::kThreads) {
     const int col = e / (D / 4), d = e % (D / 4) * 4;
     float M = -INFINITY;
 #pragma unroll
@@ -828,7 +831,7 @@ __global__ void __launch_bounds__(256, NT == 1 && FMT ? 2 : 1)
   else
     __syncthreads();
   // ---- this rank's share of the outputs, the ranks added in order
-  for (int e = rank * share + threadIdx.x; e < min(quads, (rank + 1) * share); e += 256) {
+  for (int e = rank * share + threadIdx.x; e < min(quads, (rank + 1) * share); e += C::kThreads) {
     const int col = e / (D / 4), d = e % (D / 4) * 4;
     float M = -INFINITY, L = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
     for (int r = 0; r < csize; ++r) M = fmaxf(M, gmax[r * C::kCols + col]);
@@ -879,7 +882,11 @@ int decode_nt(const CacheAttnParams& p) {
   const int64_t cols = (int64_t)p.c.max_rows * (p.Hq / p.c.Hkv);
   return p.c.fmt || cols <= 8 ? 1 : cols <= 16 ? 2 : 3;
 }
-DecPlan decode_plan(const CacheAttnParams& p, int nt, int keys_per_stage) {
+// Warps of a CTA.  bf16 pages, 8 columns: 4, two CTAs an SM, which fills the SMs more evenly (32 windowed streams
+// 51 -> 44 us); wider tiles: 8 (16 x 5 rows: 27 us, 37 with 4).  4-bit pages: 8, two CTAs an SM (four CTAs of 4
+// warps: 132 -> 134 us for 32 ragged streams, 9.6 -> 11.5 us for one).
+constexpr int decode_warps(int fmt, int nt) { return fmt == 0 && nt == 1 ? 4 : 8; }
+DecPlan decode_plan(const CacheAttnParams& p, int nt, int keys_per_stage, int warps) {
   const int64_t G = p.Hq / p.c.Hkv, cols = 8 * nt;
   const int64_t keys = p.window > 0 ? std::min<int64_t>(p.c.max_len, (int64_t)p.window + p.sinks + 8) : p.c.max_len;
   DecPlan d;
@@ -889,35 +896,35 @@ DecPlan decode_plan(const CacheAttnParams& p, int nt, int keys_per_stage) {
   // Enough CTAs to fill the SMs (4-bit: two each), as long as a warp still gets a stage (measured: one more doubling
   // costs 5-30%, one less leaves SMs idle).  16, beyond the portable cluster size, starts slowly and pays only for
   // one long sequence (131072 positions, 8 KV heads: 101 -> 79 us; 4096 positions: 8.9 -> 11 us).
-  const int slots = (p.c.fmt ? 2 : 1) * 152;
+  const int slots = (p.c.fmt ? 16 : 8) / warps * 152;
   d.cs = 1;
   // (bf16: one CTA an SM, so a doubling that starts a second wave gains nothing)
   auto more = [&](int64_t ctas) { return p.c.fmt ? ctas < slots : ctas * 2 < slots || ctas * 20 < slots * 11; };
-  while (d.cs < 8 && more(d.groups * d.cs) && (int64_t)d.cs * 8 < d.units) d.cs *= 2;
+  while (d.cs < 8 && more(d.groups * d.cs) && (int64_t)d.cs * warps < d.units) d.cs *= 2;
   if (d.cs == 8 && d.groups * 8 < 152 && d.units >= 1024) d.cs = 16;
   return d;
 }
 
-template <int D, int FMT, int NT, int F32>
+template <int D, int FMT, int NT, int F32, int W>
 cudaError_t launch_decode_t(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnParams& p,
                             cudaStream_t s) {
-  using C = DecCfg<D, FMT, NT, F32>;
+  using C = DecCfg<D, FMT, NT, F32, W>;
   static DeviceOnce once;
   cudaError_t e = device_once(once, [] {
-    cudaError_t r = cudaFuncSetAttribute(k_cache_decode<D, FMT, NT, F32>,
+    cudaError_t r = cudaFuncSetAttribute(k_cache_decode<D, FMT, NT, F32, W>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (r) return r;
-    return cudaFuncSetAttribute(k_cache_decode<D, FMT, NT, F32>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    return cudaFuncSetAttribute(k_cache_decode<D, FMT, NT, F32, W>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   });
   if (e) return e;
-  const DecPlan d = decode_plan(p, NT, C::kKeys);
+  const DecPlan d = decode_plan(p, NT, C::kKeys, W);
   const int64_t tiles = ((int64_t)p.c.max_rows * (p.Hq / p.c.Hkv) + C::kCols - 1) / C::kCols;
   const int cs = d.cs;
   if (tiles * cs > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const int sorted = p.c.n_seq > 1 && p.c.n_seq <= kSortMax && d.groups * cs > 152 ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * cs), p.c.Hkv, p.c.n_seq);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -927,7 +934,7 @@ cudaError_t launch_decode_t(const CUtensorMap& mk, const CUtensorMap& mv, const 
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_cache_decode<D, FMT, NT, F32>, mk, mv, p, cs, sorted);
+  return cudaLaunchKernelEx(&cfg, k_cache_decode<D, FMT, NT, F32, W>, mk, mv, p, cs, sorted);
 }
 
 template <int D, int FMT, int F32>
@@ -935,21 +942,22 @@ cudaError_t launch_decode_n(const CUtensorMap& mk, const CUtensorMap& mv, const 
                             cudaStream_t s) {
   const int nt = decode_nt(p);
   if constexpr (FMT == 0) {
-    if (nt == 3) return launch_decode_t<D, FMT, 3, F32>(mk, mv, p, s);
-    if (nt == 2) return launch_decode_t<D, FMT, 2, F32>(mk, mv, p, s);
+    if (nt == 3) return launch_decode_t<D, FMT, 3, F32, decode_warps(FMT, 3)>(mk, mv, p, s);
+    if (nt == 2) return launch_decode_t<D, FMT, 2, F32, decode_warps(FMT, 2)>(mk, mv, p, s);
   }
-  return launch_decode_t<D, FMT, 1, F32>(mk, mv, p, s);
+  return launch_decode_t<D, FMT, 1, F32, decode_warps(FMT, 1)>(mk, mv, p, s);
 }
 
 }  // namespace
 
 // Measured as cache_prompt_us: start and end of a CTA, and a stage of a warp (the SM full).
 float cache_decode_us(const CacheAttnParams& p) {
-  const DecPlan d = decode_plan(p, decode_nt(p), p.c.fmt ? kKvPage : kKvPage / 2);
-  const int slots = (p.c.fmt ? 2 : 1) * 152;
+  const int nt = decode_nt(p), warps = decode_warps(p.c.fmt, nt);
+  const DecPlan d = decode_plan(p, nt, p.c.fmt ? kKvPage : kKvPage / 2, warps);
+  const int slots = (p.c.fmt ? 16 : 8) / warps * 152;
   const int64_t waves = (d.groups * d.cs + slots - 1) / slots;
   const float stage = p.c.fmt ? (p.c.D == 128 ? 2.05f : 1.15f) : (p.c.D == 128 ? 1.3f : 1.05f);
-  return static_cast<float>(waves) * ((p.c.fmt ? 6.f : 5.f) + stage * static_cast<float>((d.units + 8 * d.cs - 1) / (8 * d.cs)));
+  return static_cast<float>(waves) * ((p.c.fmt ? 6.f : 5.f) + stage * static_cast<float>((d.units + warps * d.cs - 1) / (warps * d.cs)));
 }
 
 cudaError_t launch_cache_decode(const CacheAttnParams& p, cudaStream_t s) {
