@@ -29,13 +29,14 @@
 //     split in f16 hi + lo (22 bits); the probability times V's row scale is
 //     split the same way against a running reference (see below).  bf16 pages:
 //     three bf16 parts (24 bits) for float32 rows.
-//   * The maximum m (and, for 4-bit pages, the reference A of the outputs) is
-//     replaced only when a score exceeds it by more than 2^8, which one vote per
-//     page finds: in the steady state a page needs no shuffles.
+//   * The reference that a column's weights are relative to is replaced only when
+//     they grow past a bound, which one vote per page finds: in the steady state a
+//     page needs no shuffles.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "cache.cuh"
 #include "common.cuh"
@@ -48,16 +49,40 @@ namespace tf {
 namespace {
 
 constexpr int kSortMax = 256;  // sequences that a CTA puts in order of length
-constexpr float kGrow = 8.0f;  // log2 of the growth at which a reference is replaced
-// 4-bit pages: the weights p * (V's row scale) are multiplied in f16 parts, relative to a reference 2^A
-// that puts the largest at 2^7 when it is set and lets it grow to 2^15.
-constexpr float kRefBits = 7.0f, kRefTop = 15.0f;
-constexpr float kTiny = 1.92592994e-34f;  // 2^-112: weights below it count as zero
+// The weights of a column are 2^(score - ref).  bf16 pages: ref is a maximum, replaced when a score exceeds it by
+// more than kGrow (log2).  4-bit pages: the weights times V's row scales are multiplied in f16 parts, so ref puts the
+// largest such product at 2^kRefBits when it is set and is replaced when one exceeds 2^kRefTop; it is no further than
+// kRefMost below the largest score, so that the weights themselves stay far from overflow (V rows below 1e-24 lose
+// bits to that).
+constexpr float kGrow = 8.0f, kRefBits = 7.0f, kRefTop = 15.0f, kRefMost = 100.0f;
 
 __device__ __forceinline__ float ex2f(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ uint64_t pair2(float a, float b) {  // two floats, one operand of the packed instructions
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpair2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 __device__ __forceinline__ float lg2f(float x) {
   float y;
@@ -190,8 +215,8 @@ struct DecCfg {
   // what the cluster's ranks send to this CTA: [rank][its share of the outputs], [rank][col] maxima and sums
   static constexpr size_t kOffC = kOffQ + (size_t)NT * kQp * kSteps * 32 * 8;
   static constexpr size_t kOffStat = kOffC + (size_t)(kCols * D / 4 + kMaxRanks) * 16 + 2 * kMaxRanks * kCols * 4;
-  // per warp and column: reference of the outputs, maximum, sum; per column: the queries' scale
-  static constexpr size_t kOffBar = kOffStat + (size_t)(3 * kWarps + 1) * kCols * 4;
+  // per warp and column: reference, sum; per column: the queries' scale
+  static constexpr size_t kOffBar = kOffStat + (size_t)(2 * kWarps + 1) * kCols * 4;
   static constexpr size_t kSmem = 1024 + kOffBar + kWarps * kStages * 8 + 16;
 };
 
@@ -253,8 +278,7 @@ __global__ void __launch_bounds__(32 * W, DecCfg<D, FMT, NT, F32, W>::kPerSm)
   float* gpart = reinterpret_cast<float*>(smem + C::kOffC);      // from the ranks
   float* gmax = gpart + C::kCols * D + 4 * C::kMaxRanks;        // [rank][col]
   float* gsum = gmax + C::kMaxRanks * C::kCols;
-  float* wref = reinterpret_cast<float*>(smem + C::kOffStat);   // [warp][col]
-  float* wmax = wref + C::kWarps * C::kCols;
+  float* wmax = reinterpret_cast<float*>(smem + C::kOffStat);   // [warp][col]: references
   float* wsum = wmax + C::kWarps * C::kCols;
   float* qscale = wsum + C::kWarps * C::kCols;                  // [col]
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar) + warp * C::kStages;
@@ -372,22 +396,19 @@ __global__ void __launch_bounds__(32 * W, DecCfg<D, FMT, NT, F32, W>::kPerSm)
 
   // ---- this lane's columns 2 lt, 2 lt + 1 of every n-tile
   int pos[NT][2], low[NT][2];
-  float cs[NT][2], m[NT][2], mref[NT][2], l[NT][2];
-  float A[NT][2], F[NT][2], thr[NT][2];  // FMT 1: reference of the outputs
+  float cs[NT][2], ref[NT][2], l[NT][2];
   float o[NT][MT][4];
+  bool unset = true;  // some column of this lane has no reference yet
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int col = n * 8 + 2 * lt + e;
-      pos[n][e] = col < ncol ? first + (c0 + col) / G : -1;
+      pos[n][e] = col < ncol ? first + (c0 + col) / G : posmax;  // (a column that is not there sees what the last does)
       low[n][e] = win ? max(0, pos[n][e] - p.window + 1) : 0;
       cs[n][e] = qscale[col];
-      m[n][e] = -INFINITY;
-      mref[n][e] = l[n][e] = 0.f;
-      A[n][e] = -INFINITY;
-      F[n][e] = 0.f;
-      thr[n][e] = kTiny;
+      ref[n][e] = -INFINITY;
+      l[n][e] = 0.f;
     }
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -527,109 +548,115 @@ __global__ void __launch_bounds__(32 * W, DecCfg<D, FMT, NT, F32, W>::kPerSm)
         dead |= poison;
       }
 
-      // ---- softmax
-      float kscale[KB], vscale[KB];
-#pragma unroll
-      for (int bt = 0; bt < KB; ++bt) {
-        kscale[bt] = FMT ? reinterpret_cast<const float*>(Ks + Kv4<D>::kRows)[key_of(bt)] : 1.f;
-        vscale[bt] = FMT ? reinterpret_cast<const float*>(Vs + Kv4<D>::kRows)[key_of(bt)] : 1.f;
-      }
+      // ---- softmax: weights 2^(score - ref), times V's row scale (4-bit pages)
       float z[NT][KB][2];
-      bool grow = false;
+      // false, and nothing changed: a reference has to be replaced first (asked only where `checked`)
+      auto weights = [&](auto mask_, bool checked) -> bool {
+        constexpr bool kMask = decltype(mask_)::value;
+        bool again = unset;
+        uint64_t sum2[NT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
+          const uint64_t cs2 = pair2(cs[n][0], cs[n][1]);
+          const uint64_t nref2 = pair2(ref[n][0] == -INFINITY ? 0.f : -ref[n][0], ref[n][1] == -INFINITY ? 0.f : -ref[n][1]);
+          sum2[n] = pair2(l[n][0], l[n][1]);
+          float top[2] = {0.f, 0.f};
 #pragma unroll
-        for (int bt = 0; bt < KB; ++bt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float t = sc[n][bt >> 1][(bt & 1) * 2 + e] * cs[n][e];
-            if constexpr (FMT == 1) t *= kscale[bt];
-            if (!whole) {
-              const int j = j0 + key_of(bt);
-              if (!(j <= pos[n][e] && (j >= low[n][e] || j < sinks))) t = -INFINITY;
+          for (int bt = 0; bt < KB; ++bt) {
+            uint64_t t2 = pair2(sc[n][bt >> 1][(bt & 1) * 2], sc[n][bt >> 1][(bt & 1) * 2 + 1]);
+            float vs = 1.f, t[2], w[2];
+            if constexpr (FMT == 1) {
+              const float ks = reinterpret_cast<const float*>(Ks + Kv4<D>::kRows)[key_of(bt)];
+              vs = reinterpret_cast<const float*>(Vs + Kv4<D>::kRows)[key_of(bt)];
+              t2 = mul2(t2, pair2(ks, ks));
             }
-            z[n][bt][e] = t;
-            grow |= t > m[n][e] + kGrow;
-          }
-      if (__any_sync(0xFFFFFFFFu, grow)) {
+            unpair2(fma2(t2, cs2, nref2), t[0], t[1]);
+            bool on[2] = {true, true};
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+            for (int e = 0; e < 2; ++e) {
+              if constexpr (kMask) {
+                const int j = j0 + key_of(bt);
+                on[e] = j <= pos[n][e] && (j >= low[n][e] || j < sinks);
+                t[e] = on[e] ? t[e] : -INFINITY;
+              }
+              if constexpr (FMT == 0) again |= t[e] > kGrow;
+              w[e] = ex2f(t[e]);
+              if constexpr (kMask) {
+                if (((poison >> key_of(bt)) & 1u) && on[e]) w[e] = __int_as_float(0x7FFFFFFF);
+              }
+            }
+            const uint64_t w2 = pair2(w[0], w[1]);
+            sum2[n] = add2(sum2[n], w2);
+            unpair2(FMT ? mul2(w2, pair2(vs, vs)) : w2, z[n][bt][0], z[n][bt][1]);
+            if constexpr (FMT == 1) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float mx = z[n][0][e];
-#pragma unroll
-            for (int bt = 1; bt < KB; ++bt) mx = fmaxf(mx, z[n][bt][e]);
-#pragma unroll
-            for (int s = 4; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, s));
-            if (mx > m[n][e] + kGrow) {
-              const float f = m[n][e] == -INFINITY ? 0.f : ex2f(m[n][e] - mx);
-              l[n][e] *= f;
-              m[n][e] = mref[n][e] = mx;
-              if constexpr (FMT == 0) {
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                  o[n][i][e] *= f;
-                  o[n][i][2 + e] *= f;
-                }
-              } else if (A[n][e] != -INFINITY) {
-                if (mx - A[n][e] <= 120.f) {
-                  F[n][e] = ex2f(mx - A[n][e]);
-                  thr[n][e] = ex2f(A[n][e] - mx + kRefTop);
-                } else {  // nothing is left of the outputs so far
-#pragma unroll
-                  for (int i = 0; i < MT; ++i) o[n][i][e] = o[n][i][2 + e] = 0.f;
-                  A[n][e] = -INFINITY;
-                  F[n][e] = 0.f;
-                  thr[n][e] = kTiny;
-                }
+              for (int e = 0; e < 2; ++e) {
+                if constexpr (kMask) z[n][bt][e] = on[e] ? z[n][bt][e] : 0.f;  // an unseen row's scale may be anything
+                top[e] = fmaxf(top[e], z[n][bt][e]);
               }
             }
           }
-      }
-      bool wide = false;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int bt = 0; bt < KB; ++bt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float pr = ex2f(z[n][bt][e] - mref[n][e]);
-            if (poison && ((poison >> key_of(bt)) & 1u) && z[n][bt][e] != -INFINITY) pr = __int_as_float(0x7FFFFFFF);
-            l[n][e] += pr;
-            if constexpr (FMT == 1) {
-              // a masked position's row scale may be anything
-              pr = (!whole && z[n][bt][e] == -INFINITY) ? 0.f : pr * vscale[bt];
-              wide |= pr > thr[n][e];
-            }
-            z[n][bt][e] = pr;
+          if constexpr (FMT == 1) {
+            float a, b2;
+            unpair2(sum2[n], a, b2);
+            again |= fmaxf(top[0], top[1]) > 32768.f || fmaxf(a, b2) > 1.32922800e36f;  // 2^kRefTop, 2^120
           }
-      // FMT 1: the outputs' reference A (log2): they are kept divided by 2^A, so that the f16 parts of
-      // p * (V's row scale) / 2^A keep their bits whatever the size of the rows: each is off by 2^-23 of
-      // itself (two parts) or by 2^-25, half of f16's smallest step, i.e. 2^-32 of the largest weight.
-      if (FMT == 1 && __any_sync(0xFFFFFFFFu, wide)) {
+        }
+        if (checked && __any_sync(0xFFFFFFFFu, again)) return false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) unpair2(sum2[n], l[n][0], l[n][1]);
+        return true;
+      };
+      auto replace_refs = [&]() {
+        unset = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float mx = z[n][0][e];
+            float mx = -INFINITY, mw = -INFINITY;  // largest score, largest score times V's row scale (log2)
 #pragma unroll
-            for (int bt = 1; bt < KB; ++bt) mx = fmaxf(mx, z[n][bt][e]);
+            for (int bt = 0; bt < KB; ++bt) {
+              const int j = j0 + key_of(bt);
+              float t = sc[n][bt >> 1][(bt & 1) * 2 + e];
+              if constexpr (FMT == 1) t *= reinterpret_cast<const float*>(Ks + Kv4<D>::kRows)[key_of(bt)];
+              t *= cs[n][e];
+              if (whole || (j <= pos[n][e] && (j >= low[n][e] || j < sinks))) {
+                mx = fmaxf(mx, t);
+                if constexpr (FMT == 1)
+                  mw = fmaxf(mw, t + lg2f(reinterpret_cast<const float*>(Vs + Kv4<D>::kRows)[key_of(bt)]));
+              }
+            }
 #pragma unroll
-            for (int s = 4; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, s));
-            if (mx > thr[n][e]) {
-              const float An = mref[n][e] + lg2f(mx) - kRefBits;
-              const float f = A[n][e] == -INFINITY ? 0.f : ex2f(A[n][e] - An);
+            for (int s = 4; s < 32; s <<= 1) {
+              mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, s));
+              if constexpr (FMT == 1) mw = fmaxf(mw, __shfl_xor_sync(0xFFFFFFFFu, mw, s));
+            }
+            const float r = FMT ? fmaxf(mw - kRefBits, mx - kRefMost) : mx;
+            if (r > (ref[n][e] == -INFINITY ? ref[n][e] : ref[n][e] + (FMT ? kRefTop - kRefBits : kGrow))) {
+              const float f = ref[n][e] == -INFINITY ? 0.f : ex2f(ref[n][e] - r);
+              ref[n][e] = r;
+              l[n][e] *= f;
 #pragma unroll
               for (int i = 0; i < MT; ++i) {
                 o[n][i][e] *= f;
                 o[n][i][2 + e] *= f;
               }
-              A[n][e] = An;
-              F[n][e] = ex2f(mref[n][e] - An);
-              thr[n][e] = ex2f(An - mref[n][e] + kRefTop);
             }
+            unset |= ref[n][e] == -INFINITY;
           }
-      }
+      };
+      // FMT 1: each weight's f16 parts are off by 2^-23 of it (two parts) or by 2^-25, half of f16's smallest step,
+      // i.e. 2^-32 of the largest weight.
+      auto soft = [&](auto mask_) {
+        for (int turn = 0; turn < 2; ++turn) {
+          if (weights(mask_, turn == 0)) break;
+          replace_refs();
+        }
+      };
+      if (whole)
+        soft(std::integral_constant<bool, false>{});
+      else
+        soft(std::integral_constant<bool, true>{});
       // ---- probabilities as the second product's column operand: block bt holds (key, column) pairs as the
       // first product left them; the transpose gives (column, key pair)
       uint32_t pb[NT][C::kPp][KB];
@@ -639,7 +666,7 @@ __global__ void __launch_bounds__(32 * W, DecCfg<D, FMT, NT, F32, W>::kPerSm)
         for (int bt = 0; bt < KB; ++bt) {
           uint32_t part[C::kPp];
           if constexpr (FMT == 1)
-            split_pair<1, C::kPp>(z[n][bt][0] * F[n][0], z[n][bt][1] * F[n][1], part);
+            split_pair<1, C::kPp>(z[n][bt][0], z[n][bt][1], part);
           else
             split_pair<0, C::kPp>(z[n][bt][0], z[n][bt][1], part);
 #pragma unroll
@@ -765,8 +792,7 @@ __global__ void __launch_bounds__(32 * W, DecCfg<D, FMT, NT, F32, W>::kPerSm)
         }
       }
       if (lg == 0) {
-        wref[warp * C::kCols + col] = FMT ? A[n][e] : m[n][e];
-        wmax[warp * C::kCols + col] = m[n][e];
+        wmax[warp * C::kCols + col] = ref[n][e];
         wsum[warp * C::kCols + col] = l[n][e];
       }
     }
@@ -801,7 +827,7 @@ __global__ void __launch_bounds__(32 * W, DecCfg<D, FMT, NT, F32, W>::kPerSm)
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < C::kWarps; ++w) {
-      const float rw = wref[w * C::kCols + col];
+      const float rw = wmax[w * C::kCols + col];
       const float f = rw == -INFINITY ? 0.f : ex2f(rw - M);
       const float* wp = wpart + (size_t)w * C::kPartFloats;
       float4 v;
