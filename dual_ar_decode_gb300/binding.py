@@ -78,6 +78,7 @@ EXPORTS = {
                                          ctypes.POINTER(ctypes.c_int64)]),
     "tf_prefill_seq": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32]),
     "tf_release_seq": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32]),
+    "tf_fork_seq": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32]),
     "tf_test_inject": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32]),
     "tf_test_fail_alloc": (None, [ctypes.c_int32]),
     "tf_op_quantize_fp8": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
@@ -266,6 +267,12 @@ class Decoder:
         _check(lib().tf_release_seq(self.h, slot), self.h)
         self.active = getattr(self, "active", set()) - {slot}
         self.batch = max(self.active) + 1 if self.active else 1
+
+    def fork_seq(self, src: int, dst: int):
+        """Make slot `dst` a second copy of the sequence in slot `src`; both decode on."""
+        _check(lib().tf_fork_seq(self.h, src, dst), self.h)
+        self.active = getattr(self, "active", set()) | {dst}
+        self.batch = max(self.active) + 1
 
     def decode_frame(self, sampling=None, forced=None, logits=False):
         B = self.batch

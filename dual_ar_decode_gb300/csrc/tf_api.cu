@@ -187,6 +187,7 @@ struct tf_ctx {
   int32_t* kv_tbl = nullptr;
   std::vector<int32_t> tbl_host;
   std::vector<int32_t> free_pages;
+  std::vector<int32_t> page_refs;  // slots that hold a page (full pages of forked sequences are shared)
   std::vector<int32_t> seq_pages[kMaxBatch];
 
   cudaGraphExec_t graph[2] = {nullptr, nullptr};  // [0] greedy, [1] top-k
@@ -319,6 +320,7 @@ tf_status ensure_pages(tf_ctx* c, int slot, int last) {
     if (c->free_pages.empty()) return fail(c, TF_E_CAPACITY, "no free KV page");
     const int32_t pg = c->free_pages.back();
     c->free_pages.pop_back();
+    c->page_refs[pg] = 1;
     c->tbl_host[(size_t)slot * c->npp + mine.size()] = pg;
     mine.push_back(pg);
   }
@@ -327,7 +329,7 @@ tf_status ensure_pages(tf_ctx* c, int slot, int last) {
   return TF_OK;
 }
 
-// Frees slot `slot`: its pages go back to the free list (its block-table row
+// Frees slot `slot`: its pages, unless another slot shares them, go back to the free list (its block-table row
 // points at the scratch page 0 again) and its state is cleared on the host.
 tf_status release_slot(tf_ctx* c, int slot) {
   c->active_host[slot] = 0;
@@ -337,7 +339,8 @@ tf_status release_slot(tf_ctx* c, int slot) {
   if (!c->paged) return TF_OK;
   std::vector<int32_t>& mine = c->seq_pages[slot];
   if (mine.empty()) return TF_OK;
-  for (size_t i = mine.size(); i-- > 0;) c->free_pages.push_back(mine[i]);
+  for (size_t i = mine.size(); i-- > 0;)
+    if (--c->page_refs[mine[i]] == 0) c->free_pages.push_back(mine[i]);
   mine.clear();
   std::fill(c->tbl_host.begin() + (size_t)slot * c->npp, c->tbl_host.begin() + (size_t)(slot + 1) * c->npp, 0);
   CK(cudaMemcpyAsync(c->kv_tbl + (size_t)slot * c->npp, c->tbl_host.data() + (size_t)slot * c->npp,
@@ -1322,6 +1325,7 @@ tf_status tf_create(const tf_config* cfg, int device, tf_ctx** out) {
   if (c->paged) {
     if (dev_alloc_t(c, &c->kv_tbl, B * c->npp)) return bail(TF_E_NOMEM);
     c->tbl_host.assign(B * c->npp, 0);
+    c->page_refs.assign(n_pages, 0);
     for (size_t pg = n_pages - 1; pg >= 1; --pg) c->free_pages.push_back(static_cast<int32_t>(pg));
   }
   const size_t fkv = B * kv_elems;  // fast uses positions 0..9 of a T-slot cache
@@ -1699,6 +1703,85 @@ tf_status tf_release_seq(tf_ctx* c, int32_t slot) {
   if ((r = upload_slots(c))) return r;
   CK(cudaStreamSynchronize(c->stream));
   c->Bc = std::max(1, slots_in_use(c));
+  return TF_OK;
+}
+
+// Copies positions 0..n-1 of slot src's slow caches to slot dst: with page pools the one page that both would go on
+// writing (the full ones are shared), else every cached row, in units of as many rows as divide a slab.
+static cudaError_t fork_caches(tf_ctx* c, int src, int dst, int n) {
+  std::vector<void*> pools;
+  for (const Layer& L : c->slow) {
+    pools.push_back(L.K);
+    pools.push_back(L.V);
+  }
+  std::vector<int32_t> from, to;
+  int unit = kKvPage;
+  int64_t bytes = 0;
+  if (c->paged) {
+    bytes = (int64_t)c->Hkv * kKvPage * c->D * 2;
+    if (n % kKvPage) {
+      from.push_back(c->seq_pages[src][n / kKvPage]);
+      to.push_back(c->seq_pages[dst][n / kKvPage]);
+    }
+  } else {
+    while (c->T % unit) unit /= 2;
+    bytes = (int64_t)unit * c->D * 2;
+    for (int g = 0; g < c->Hkv; ++g)
+      for (int i = 0; i < (n + unit - 1) / unit; ++i) {
+        from.push_back((int32_t)(((int64_t)src * c->Hkv + g) * (c->T / unit) + i));
+        to.push_back((int32_t)(((int64_t)dst * c->Hkv + g) * (c->T / unit) + i));
+      }
+  }
+  if (from.empty()) return cudaSuccess;
+  return launch_cache_copy(pools.data(), static_cast<int>(pools.size()), bytes, from.data(), to.data(),
+                           static_cast<int>(from.size()), c->stream);
+}
+
+tf_status tf_fork_seq(tf_ctx* c, int32_t src, int32_t dst) {
+  if (!c) return TF_E_INVAL;
+  if (c->poisoned) return fail(c, TF_E_STATE, "context poisoned by an earlier error");
+  if (src < 0 || src >= c->Bmax || dst < 0 || dst >= c->Bmax || src == dst)
+    return fail(c, TF_E_INVAL, "src and dst must be two slots in [0, max_batch)");
+  if (!c->active_host[src]) return fail(c, TF_E_STATE, "no sequence in slot " + std::to_string(src));
+  CK(cudaSetDevice(c->device));
+  const int n = c->pos_host[src];
+  tf_status r;
+  if ((r = release_slot(c, dst))) return r;
+  if (c->paged) {
+    // full pages are never written again: both slots hold them
+    for (int i = 0; i < n / kKvPage; ++i) {
+      const int32_t pg = c->seq_pages[src][i];
+      ++c->page_refs[pg];
+      c->seq_pages[dst].push_back(pg);
+      c->tbl_host[(size_t)dst * c->npp + i] = pg;
+    }
+    // (a slot holds at most npp pages and the pool has npp for each, so one is free for the last page)
+    if (n % kKvPage) {
+      if ((r = ensure_pages(c, dst, n - 1))) {
+        release_slot(c, dst);
+        return r;
+      }
+    } else if (n) {
+      CK(cudaMemcpyAsync(c->kv_tbl + (size_t)dst * c->npp, c->tbl_host.data() + (size_t)dst * c->npp,
+                         sizeof(int32_t) * c->npp, cudaMemcpyHostToDevice, c->stream));
+    }
+  }
+  CK(fork_caches(c, src, dst, n));
+  // the ids fed back last and the repetition window's ring
+  CK(cudaMemcpyAsync(c->st->fb + dst * kIdStride, c->st->fb + src * kIdStride, sizeof(int32_t) * kIdStride,
+                     cudaMemcpyDeviceToDevice, c->stream));
+  CK(cudaMemcpyAsync(c->st->sel + dst * kIdStride, c->st->sel + src * kIdStride, sizeof(int32_t) * kIdStride,
+                     cudaMemcpyDeviceToDevice, c->stream));
+  CK(cudaMemcpyAsync(c->fb_ring + (size_t)dst * kRepRing * kRepIds, c->fb_ring + (size_t)src * kRepRing * kRepIds,
+                     sizeof(int32_t) * kRepRing * kRepIds, cudaMemcpyDeviceToDevice, c->stream));
+  c->pos_host[dst] = n;
+  c->frame_host[dst] = c->frame_host[src];
+  c->active_host[dst] = 1;
+  c->pending_host[dst] = c->pending_host[src];
+  if ((r = upload_slots(c))) return r;
+  CK(cudaStreamSynchronize(c->stream));
+  c->Bc = slots_in_use(c);
+  c->uniform = false;
   return TF_OK;
 }
 

@@ -215,6 +215,18 @@ tf_status tf_prefill_seq(tf_ctx* ctx, int32_t slot, const int32_t* tokens, int32
  * and, with paged caches, its pages return to the pool.  Errors: TF_E_INVAL. */
 tf_status tf_release_seq(tf_ctx* ctx, int32_t slot);
 
+/* Forks a sequence: slot dst becomes a second copy of the sequence in slot
+ * src, at the same position, with the same fed-back ids, repetition window
+ * and frame index (several takes of one prompt, which the sampling draws tell
+ * apart by their slot: the Philox counter's third word).  A sequence already
+ * in dst is released first.  With TF_FLAG_PAGED_KV the two share every full
+ * page of the past and only the last, partly filled one is copied (see
+ * tf_op_cache_copy); with dense caches the cached rows are copied.  Both then
+ * decode on their own.  (The pages name continuous batching with a paged KV
+ * cache without details; a fork has no counterpart there.)
+ * Errors: TF_E_INVAL (slots), TF_E_STATE (no sequence in src), TF_E_CUDA. */
+tf_status tf_fork_seq(tf_ctx* ctx, int32_t src, int32_t dst);
+
 /* One decode frame: feeds each active sequence's last codebook-0 id (or the
  * last id of a prompt started with tf_prefill_seq) at its own next position
  * and emits the next frame of every slot up to the last active one (B =
