@@ -563,14 +563,15 @@ __global__ void __launch_bounds__(32 * W, DecCfg<D, FMT, NT, F32, W>::kPerSm)
           float top[2] = {0.f, 0.f};
 #pragma unroll
           for (int bt = 0; bt < KB; ++bt) {
-            uint64_t t2 = pair2(sc[n][bt >> 1][(bt & 1) * 2], sc[n][bt >> 1][(bt & 1) * 2 + 1]);
+            const uint64_t s2 = pair2(sc[n][bt >> 1][(bt & 1) * 2], sc[n][bt >> 1][(bt & 1) * 2 + 1]);
             float vs = 1.f, t[2], w[2];
-            if constexpr (FMT == 1) {
+            if constexpr (FMT == 1) {  // the queries' scale first: it undoes what scaled them up
               const float ks = reinterpret_cast<const float*>(Ks + Kv4<D>::kRows)[key_of(bt)];
               vs = reinterpret_cast<const float*>(Vs + Kv4<D>::kRows)[key_of(bt)];
-              t2 = mul2(t2, pair2(ks, ks));
+              unpair2(fma2(mul2(s2, cs2), pair2(ks, ks), nref2), t[0], t[1]);
+            } else {
+              unpair2(fma2(s2, cs2, nref2), t[0], t[1]);
             }
-            unpair2(fma2(t2, cs2, nref2), t[0], t[1]);
             bool on[2] = {true, true};
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -617,9 +618,8 @@ __global__ void __launch_bounds__(32 * W, DecCfg<D, FMT, NT, F32, W>::kPerSm)
 #pragma unroll
             for (int bt = 0; bt < KB; ++bt) {
               const int j = j0 + key_of(bt);
-              float t = sc[n][bt >> 1][(bt & 1) * 2 + e];
+              float t = sc[n][bt >> 1][(bt & 1) * 2 + e] * cs[n][e];
               if constexpr (FMT == 1) t *= reinterpret_cast<const float*>(Ks + Kv4<D>::kRows)[key_of(bt)];
-              t *= cs[n][e];
               if (whole || (j <= pos[n][e] && (j >= low[n][e] || j < sinks))) {
                 mx = fmaxf(mx, t);
                 if constexpr (FMT == 1)
@@ -947,7 +947,8 @@ cudaError_t launch_decode_t(const CUtensorMap& mk, const CUtensorMap& mv, const 
   const int64_t tiles = ((int64_t)p.c.max_rows * (p.Hq / p.c.Hkv) + C::kCols - 1) / C::kCols;
   const int cs = d.cs;
   if (tiles * cs > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  const int sorted = p.c.n_seq > 1 && p.c.n_seq <= kSortMax && d.groups * cs > 152 ? 1 : 0;
+  // (CTAs that all fit at once need no order)
+  const int sorted = p.c.n_seq > 1 && p.c.n_seq <= kSortMax && d.groups * cs > C::kPerSm * 152 ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * cs), p.c.Hkv, p.c.n_seq);
   cfg.blockDim = dim3(C::kThreads);

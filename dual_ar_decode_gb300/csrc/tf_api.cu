@@ -1737,8 +1737,7 @@ static cudaError_t fork_caches(tf_ctx* c, int src, int dst, int n) {
                            static_cast<int>(from.size()), c->stream);
 }
 
-tf_status tf_fork_seq(tf_ctx* c, int32_t src, int32_t dst) {
-  if (!c) return TF_E_INVAL;
+static tf_status fork_slot(tf_ctx* c, int32_t src, int32_t dst) {
   if (c->poisoned) return fail(c, TF_E_STATE, "context poisoned by an earlier error");
   if (src < 0 || src >= c->Bmax || dst < 0 || dst >= c->Bmax || src == dst)
     return fail(c, TF_E_INVAL, "src and dst must be two slots in [0, max_batch)");
@@ -1757,10 +1756,7 @@ tf_status tf_fork_seq(tf_ctx* c, int32_t src, int32_t dst) {
     }
     // (a slot holds at most npp pages and the pool has npp for each, so one is free for the last page)
     if (n % kKvPage) {
-      if ((r = ensure_pages(c, dst, n - 1))) {
-        release_slot(c, dst);
-        return r;
-      }
+      if ((r = ensure_pages(c, dst, n - 1))) return r;
     } else if (n) {
       CK(cudaMemcpyAsync(c->kv_tbl + (size_t)dst * c->npp, c->tbl_host.data() + (size_t)dst * c->npp,
                          sizeof(int32_t) * c->npp, cudaMemcpyHostToDevice, c->stream));
@@ -1783,6 +1779,16 @@ tf_status tf_fork_seq(tf_ctx* c, int32_t src, int32_t dst) {
   c->Bc = slots_in_use(c);
   c->uniform = false;
   return TF_OK;
+}
+
+tf_status tf_fork_seq(tf_ctx* c, int32_t src, int32_t dst) {
+  if (!c) return TF_E_INVAL;
+  try {
+    return fork_slot(c, src, dst);
+  } catch (const std::bad_alloc&) {  // slot dst may be half set up: nothing of it is used
+    c->poisoned = true;
+    return TF_E_NOMEM;
+  }
 }
 
 // Checks that every active slot can take n more frames and gives the paged
