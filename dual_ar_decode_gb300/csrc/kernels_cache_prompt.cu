@@ -93,6 +93,19 @@ __device__ __forceinline__ bool bar_wait_warp(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity) ? 1 : 0) != 0;
 }
 
+__device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_store3(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
@@ -229,7 +242,11 @@ __device__ __forceinline__ uint4* chunk_at(uint8_t* tile, int r, int ch) {
 }
 
 // Bits of the 32 positions from base that a row at `pos` sees.
-__device__ __forceinline__ uint32_t ones(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
+__device__ __forceinline__ uint32_t ones(int n) {  // the n lowest bits; none below 0, all from 32 on
+  uint32_t d;
+  asm("bmsk.clamp.b32 %0, %1, %2;" : "=r"(d) : "r"(0), "r"(max(n, 0)));
+  return d;
+}
 __device__ __forceinline__ uint32_t sees(int base, int pos, int low, int sinks) {
   return ones(pos - base + 1) & (~ones(low - base) | ones(sinks - base));
 }
@@ -237,7 +254,8 @@ __device__ __forceinline__ uint32_t sees(int base, int pos, int low, int sinks) 
 template <int D, int FMT, int NX>
 __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
     k_cache_prompt(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                   const CacheAttnParams p) {
+                   const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_o,
+                   const CacheAttnParams p, const int boxed) {
   constexpr int span = 128 * NX;  // pairs of the CTA: NX tiles
   using C = PromptCfg<D, FMT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -272,6 +290,10 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
   const int pages = posmax < 0 ? 0 : psink + posmax / kKvPage - plow + 1;
   const int nt = (pages + 3) / 4;
   auto base_at = [&](int u) { return (u < psink ? u : plow + u - psink) * kKvPage; };
+  // Tiles are taken from the second on and the first last: with a window the first is masked, and the pipeline
+  // starts faster on one that is not.
+  const int turn = win && nt >= 3 ? 1 : 0;
+  auto tile_at = [&](int j) { return j + turn < nt ? j + turn : j + turn - nt; };
   auto quarter_whole = [&](int bq) {
     return bq + kKvPage - 1 <= posmin && (bq >= lowmax || bq + kKvPage <= sinks) ? 1 : 0;
   };
@@ -295,7 +317,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
       mbar_init(&o_done[i], 1);
     }
     mbar_init(drained, 1);
-    mbar_init(q_full, 256);
+    mbar_init(q_full, boxed ? 1 : 256);
     *failed = 0;
     fence_mbar_init();
   }
@@ -318,6 +340,15 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
     // ---------------------------------------------------------------- MMA issuer
     if (lane == 0) {
       bool ok = true;
+      if (boxed) {  // pairs are consecutive (row, head) rows of Q: one box per tile and 64 columns
+        mbar_arrive_expect_tx(q_full, NX * C::kTile);
+#pragma unroll
+        for (int x = 0; x < NX; ++x)
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tma_box3(smem_u32(smem) + x * C::kTile + h * 16384, &map_q, h * 64, hkv * G,
+                     sq.r0 + (c0 + x * 128) / G, q_full);
+      }
       auto score = [&](int x, int j) {  // S_x = Q_x K(j)^T
         const uint32_t qb = smem_u32(smem) + x * C::kTile, kb = smem_u32(sk) + (j & 1) * C::kTile;
 #pragma unroll
@@ -376,7 +407,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
           uint32_t boxes = 0;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int u = 4 * j + q;
+            const int u = 4 * tile_at(j) + q;
             pg[q] = u < pages ? cache_page(c, b, base_at(u) / kKvPage) : -1;
             boxes += pg[q] >= 0 ? 1u : 0u;
           }
@@ -384,7 +415,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
           Info* in = info(j);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int bq = pg[q] >= 0 ? base_at(4 * j + q) : kNowhere;
+            const int bq = pg[q] >= 0 ? base_at(4 * tile_at(j) + q) : kNowhere;
             in->base[q] = bq;
             in->poison[q] = 0;
             in->whole[q] = quarter_whole(bq);
@@ -458,10 +489,14 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
       uint4 raw[NI];
       uint32_t ksb[NI], vsb[NI];
       bool ok = true;
-      int page = 0 < pages ? (w < pages ? cache_page(c, b, base_at(w) / kKvPage) : -1) : -1;
+      auto page_of = [&](int j) {  // of this warp's quarter of the j-th tile taken
+        const int u = 4 * tile_at(j) + w;
+        return j < nt && u < pages ? cache_page(c, b, base_at(u) / kKvPage) : -1;
+      };
+      int page = page_of(0);
       for (int j = 0; j < nt; ++j) {
-        const int s = j & 1, u = 4 * j + w;
-        const int base = page >= 0 ? base_at(u) : kNowhere;
+        const int s = j & 1;
+        const int base = page >= 0 ? base_at(4 * tile_at(j) + w) : kNowhere;
         const uint8_t* kp = c.K + ((size_t)max(page, 0) * c.Hkv + hkv) * L::kBytes;
         const uint8_t* vp = c.V + ((size_t)max(page, 0) * c.Hkv + hkv) * L::kBytes;
         float krow = 0.f, vrow = 0.f;
@@ -481,7 +516,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
           vrow = __ldg(reinterpret_cast<const float*>(vp + L::kRows) + lane);
         }
         // the next page's id, two loads ahead of its use
-        const int next = u + 4 < pages ? cache_page(c, b, base_at(u + 4) / kKvPage) : -1;
+        const int next = page_of(j + 1);
         const int whole = quarter_whole(base);
         uint32_t dead = 0, poison = 0;
         if (!whole) {
@@ -586,7 +621,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
     auto from_lane = [&](int64_t v, int src) {
       return static_cast<int64_t>(__shfl_sync(0xFFFFFFFFu, static_cast<long long>(v), src));
     };
-    {
+    if (!boxed) {
       const int64_t at = pair_at(lane / kLines * (8 * kLines) + warp * kLines + lane % kLines, p.q_stride);
 #pragma unroll 4
       for (int it = 0; it < kChunks; ++it) {
@@ -605,9 +640,11 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
         }
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    mbar_arrive(q_full);
+    if (!boxed) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(q_full);
+    }
     int pos[4], low[4];
     float ref[4], l[4];
 #pragma unroll
@@ -824,6 +861,17 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
           *chunk_at(rows, r0 + lane, (d + i) / 8) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
+      if (boxed && col0 + 32 <= ncol) {  // whole rows of the output, all of them this warp's
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tma_store3(&map_o, smem_u32(rows) + h * 16384 + r0 * 128, h * 64, hkv * G, sq.r0 + (c0 + col0) / G);
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // (shared memory is read, then the CTA may end)
+        }
+      } else {
       __syncwarp();
       const int64_t at = pair_at(col0 + lane, p.out_stride);
 #pragma unroll 4
@@ -843,6 +891,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
             }
           }
         }
+      }
       }
     } else if (!ok && lane == 0) {
       *failed = 1;
@@ -867,6 +916,20 @@ int64_t prompt_ctas(const CacheAttnParams& p, int span) {
 // 1.63 with two, bf16, D = 128, so two pay once the CTAs queue).
 int prompt_span(const CacheAttnParams& p) { return prompt_ctas(p, 128) <= 152 ? 128 : 256; }
 
+// Rows of queries or outputs as boxes of 64 columns x G heads x `rows` rows.
+bool rows_map(CUtensorMap* map, const void* base, const CacheAttnParams& p, int64_t stride, int pairs) {
+  const int G = p.Hq / p.c.Hkv;
+  EncodeTiled fn = encode_fn();
+  if (!fn || 32 % G || reinterpret_cast<uintptr_t>(base) % 16 || stride % 8 || stride >= (1ll << 38)) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)p.c.D, (cuuint64_t)p.Hq, (cuuint64_t)p.c.n_rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)p.c.D * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(pairs / G)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, int FMT, int NX>
 cudaError_t launch_prompt_x(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnParams& p,
                             cudaStream_t s) {
@@ -879,8 +942,11 @@ cudaError_t launch_prompt_x(const CUtensorMap& mk, const CUtensorMap& mv, const 
   constexpr int span = 128 * NX;
   const int64_t tiles = ((int64_t)p.c.max_rows * (p.Hq / p.c.Hkv) + span - 1) / span;
   if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  // queries and outputs by TMA where heads divide a tile's rows and everything is 16-byte aligned
+  CUtensorMap mq = {}, mo = {};
+  const int boxed = rows_map(&mq, p.q, p, p.q_stride, 128) && rows_map(&mo, p.out, p, p.out_stride, 32) ? 1 : 0;
   k_cache_prompt<D, FMT, NX><<<dim3(static_cast<unsigned>(tiles), p.c.Hkv, p.c.n_seq), C::kThreads, C::kSmem, s>>>(
-      mk, mv, p);
+      mk, mv, mq, mo, p, boxed);
   return cudaGetLastError();
 }
 
