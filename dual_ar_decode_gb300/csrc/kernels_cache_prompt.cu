@@ -241,6 +241,10 @@ __device__ __forceinline__ uint4* chunk_at(uint8_t* tile, int r, int ch) {
   return reinterpret_cast<uint4*>(tile + (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
 }
 
+__device__ __forceinline__ void st_shared16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
 // Bits of the 32 positions from base that a row at `pos` sees.
 __device__ __forceinline__ uint32_t ones(int n) {  // the n lowest bits; none below 0, all from 32 on
   uint32_t d;
@@ -495,6 +499,9 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
       };
       int page = page_of(0);
       for (int j = 0; j < nt; ++j) {
+        // (opaque to the compiler: kept across the loop, a lane's addresses would not fit its registers)
+        int ln = lane;
+        asm volatile("" : "+r"(ln));
         const int s = j & 1;
         const int base = page >= 0 ? base_at(4 * tile_at(j) + w) : kNowhere;
         const uint8_t* kp = c.K + ((size_t)max(page, 0) * c.Hkv + hkv) * L::kBytes;
@@ -538,12 +545,15 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
         }
         in->ks[w * 32 + lane] = krow * p.scale_log2;
         in->vs[w * 32 + lane] = (dead >> lane) & 1u ? 0.f : vrow;
-        uint8_t* kt = sk + s * C::kTile;
+        // Row r = w * 32 + (32 i + lane) / PR, blocks 2 q and 2 q + 1 of it: chunk x of the four lies at the first one's
+        // address ^ x * 16 (r & 7 is the same for every i).  The lanes of a row's upper half store their blocks the
+        // other way round: no bank conflicts.
+        const int q = ln % PR, r0 = ln / PR;
+        const bool swap = (q >> 1) & 1;
+        const uint32_t kt = smem_u32(sk) + s * C::kTile + (q >> 1) * 16384 + (w * 32 + r0) * 128 +
+                            ((((4 * q) & 7) ^ (r0 & 7)) << 4);
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-          const int e = i * 32 + lane, r = w * 32 + e / PR, q = e % PR;
-          // (the lanes of the row's upper half store their blocks the other way round: no bank conflicts)
-          const bool swap = (q >> 1) & 1;
           const uint32_t words[4] = {swap ? raw[i].z : raw[i].x, swap ? raw[i].w : raw[i].y,
                                      swap ? raw[i].x : raw[i].z, swap ? raw[i].y : raw[i].w};
           const uint32_t s2 = e4m3x2_f16(swap ? __byte_perm(ksb[i], 0, 0x4401) : ksb[i]);
@@ -557,7 +567,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
               const float2 f = scaled(h[y], sd);
               o[y] = pack_bf16(f.x, f.y);
             }
-            *chunk_at(kt, r, 4 * q + (x ^ (swap ? 2 : 0))) = make_uint4(o[0], o[1], o[2], o[3]);
+            st_shared16((kt ^ ((x ^ (swap ? 2 : 0)) << 4)) + i * (32 / PR) * 128, o[0], o[1], o[2], o[3]);
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -566,14 +576,16 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
         for (int i = 0; i < NI; ++i)
           if (page >= 0) raw[i] = __ldg(reinterpret_cast<const uint4*>(vp + v_unit(i) * 16));
         if (j >= 2 && !(ok = bar_wait_warp(&v_empty[s], ((j >> 1) - 1) & 1))) break;
-        uint8_t* vt = sv + s * C::kTile;
         dead |= poison;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-          const int v = v_unit(i), r = v_row(v), blk = (v % (D / 4)) / 4, row = w * 32 + r;
-          const bool swap = blk & 1;
-          const uint32_t words[4] = {swap ? raw[i].z : raw[i].x, swap ? raw[i].w : raw[i].y,
-                                     swap ? raw[i].x : raw[i].z, swap ? raw[i].y : raw[i].w};
+          // rows r and r + 1 (r even) of block blk: chunk h of row r at vt ^ h * 16, of row r + 1 at (vt + 128) ^ 16 ^ h * 16
+          const int v = D == 128 ? ((i + ln) & 3) * 32 + ln : i * 32 + ln;
+          const int r = v_row(v), blk = (v % (D / 4)) / 4;
+          const uint32_t vt = smem_u32(sv) + s * C::kTile + (blk >> 2) * 16384 + (w * 32 + r) * 128 +
+                              ((((2 * blk) & 7) ^ (r & 7)) << 4);
+          const uint32_t words[4] = {blk & 1 ? raw[i].z : raw[i].x, blk & 1 ? raw[i].w : raw[i].y,
+                                     blk & 1 ? raw[i].x : raw[i].z, blk & 1 ? raw[i].y : raw[i].w};
           uint32_t sb = vsb[i];
           if ((dead >> r) & 1u) sb &= 0xFF00u;
           if ((dead >> r) & 2u) sb &= 0x00FFu;
@@ -592,8 +604,9 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
               o0[2 + y] = pack_bf16(g0.x, g1.x);
               o1[2 + y] = pack_bf16(g0.y, g1.y);
             }
-            *chunk_at(vt, row, 2 * blk + (x / 2 ^ (swap ? 1 : 0))) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-            *chunk_at(vt, row + 1, 2 * blk + (x / 2 ^ (swap ? 1 : 0))) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+            const uint32_t h16 = (x / 2 ^ (blk & 1)) << 4;
+            st_shared16(vt ^ h16, o0[0], o0[1], o0[2], o0[3]);
+            st_shared16((vt + 128) ^ 16 ^ h16, o1[0], o1[1], o1[2], o1[3]);
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
