@@ -44,8 +44,8 @@ namespace tf {
 
 namespace {
 
-// The maximum that the exponentials are relative to is replaced when a lane's sum of a row's 32 probabilities of
-// a tile exceeds this (2^13; so no probability does).
+// The maximum that the exponentials are relative to is replaced when a lane's sum of a row's probabilities of a
+// tile or part of it exceeds this (2^13; so no probability does).
 constexpr float kMaxSum = 8192.0f;
 constexpr int kInfo = 4;         // tiles of which the position / scale records are kept
 constexpr int kNowhere = 0x3FFFFFFF;  // base position of a quarter that holds nothing
@@ -66,6 +66,9 @@ struct PromptCfg {
   // that whole warpgroups can trade registers: the softmax takes what the others do not need).
   static constexpr int kThreads = FMT ? 32 * 16 : 32 * 12;
   static constexpr int kMmaWarp = FMT ? 12 : 8;
+  // Quarters of a tile whose p a lane keeps before it stores them: what its registers hold (FMT 1, 2 x 1024 rows
+  // over 5120 positions: 219 us with 1, 199 with 2, 204 with 4, which spills).
+  static constexpr int kGroup = FMT ? 2 : 4;
   static constexpr uint32_t kCols = 512;
   // kind::f16, fp32 accumulate, bf16 operands, M = 128.  S: B = K tile, K-major, N = 128.
   // O: B = V tile, MN-major (bit 16), N = D.
@@ -154,7 +157,14 @@ __device__ __forceinline__ void tm_ld32(uint32_t addr, float (&v)[32]) {
         "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
@@ -184,7 +194,37 @@ __device__ __forceinline__ void tm_pair_st(uint32_t addr, const uint32_t (&r)[8]
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
 }
-__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_pair_ld(uint32_t addr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x128b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
+}
+// Waits for the loads; the registers go through it, so that nothing uses them before.
+__device__ __forceinline__ void tm_wait_ld(uint32_t (&r)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tm_wait_ld(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tm_wait_ld(uint32_t (&s)[2][16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(s[0][0]), "+r"(s[0][1]), "+r"(s[0][2]), "+r"(s[0][3]), "+r"(s[0][4]), "+r"(s[0][5]),
+                 "+r"(s[0][6]), "+r"(s[0][7]), "+r"(s[0][8]), "+r"(s[0][9]), "+r"(s[0][10]), "+r"(s[0][11]),
+                 "+r"(s[0][12]), "+r"(s[0][13]), "+r"(s[0][14]), "+r"(s[0][15]), "+r"(s[1][0]), "+r"(s[1][1]),
+                 "+r"(s[1][2]), "+r"(s[1][3]), "+r"(s[1][4]), "+r"(s[1][5]), "+r"(s[1][6]), "+r"(s[1][7]),
+                 "+r"(s[1][8]), "+r"(s[1][9]), "+r"(s[1][10]), "+r"(s[1][11]), "+r"(s[1][12]), "+r"(s[1][13]),
+                 "+r"(s[1][14]), "+r"(s[1][15])
+               :
+               : "memory");
+}
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t d;
@@ -339,283 +379,283 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
   // FMT 1: the softmax's warpgroups take registers from the other two: 256 x 160 + 256 x 96 = the launch's
   // 512 x 128
   if (warp >= 8) {
-  if constexpr (FMT == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-  if (warp == C::kMmaWarp) {
-    // ---------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      bool ok = true;
-      if (boxed) {  // pairs are consecutive (row, head) rows of Q: one box per tile and 64 columns
-        mbar_arrive_expect_tx(q_full, NX * C::kTile);
+    if constexpr (FMT == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    if (warp == C::kMmaWarp) {
+      // ---------------------------------------------------------------- MMA issuer
+      if (lane == 0) {
+        bool ok = true;
+        if (boxed) {  // pairs are consecutive (row, head) rows of Q: one box per tile and 64 columns
+          mbar_arrive_expect_tx(q_full, NX * C::kTile);
 #pragma unroll
-        for (int x = 0; x < NX; ++x)
+          for (int x = 0; x < NX; ++x)
 #pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            tma_box3(smem_u32(smem) + x * C::kTile + h * 16384, &map_q, h * 64, hkv * G,
-                     sq.r0 + (c0 + x * 128) / G, q_full);
-      }
-      auto score = [&](int x, int j) {  // S_x = Q_x K(j)^T
-        const uint32_t qb = smem_u32(smem) + x * C::kTile, kb = smem_u32(sk) + (j & 1) * C::kTile;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-          mma_ss(tmem + x * 128, desc_k(qb + off), desc_k(kb + off), C::kIdescS, kk > 0 ? 1u : 0u);
+            for (int h = 0; h < D / 64; ++h)
+              tma_box3(smem_u32(smem) + x * C::kTile + h * 16384, &map_q, h * 64, hkv * G,
+                       sq.r0 + (c0 + x * 128) / G, q_full);
         }
-        mma_commit(&s_full[x]);
-      };
-      if (nt > 0) {
-        ok = bar_wait(q_full, 0) && bar_wait(&k_full[0], 0);
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if (ok) {
-          score(0, 0);
-          if constexpr (NX > 1) score(1, 0);
-          mma_commit(&k_empty[0]);
-        }
-      }
-      for (int j = 0; ok && j < nt; ++j) {
+        auto score = [&](int x, int j) {  // S_x = Q_x K(j)^T
+          const uint32_t qb = smem_u32(smem) + x * C::kTile, kb = smem_u32(sk) + (j & 1) * C::kTile;
 #pragma unroll
-        for (int x = 0; x < NX; ++x) {
-          ok = ok && bar_wait(&p_full[x], j & 1) && (x || bar_wait(FMT ? &v_full[j & 1] : &v_clean[j & 1], (j >> 1) & 1));
-          if (!ok) break;
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+            mma_ss(tmem + x * 128, desc_k(qb + off), desc_k(kb + off), C::kIdescS, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(&s_full[x]);
+        };
+        if (nt > 0) {
+          ok = bar_wait(q_full, 0) && bar_wait(&k_full[0], 0);
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint32_t vb = smem_u32(sv) + (j & 1) * C::kTile;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, desc_mn(vb + kk * 2048), C::kIdescO,
-                   (j > 0 || kk > 0) ? 1u : 0u);
-          if (x == NX - 1) mma_commit(&v_empty[j & 1]);
-          if (j + 1 < nt) {
-            if (!x) {
-              ok = bar_wait(&k_full[(j + 1) & 1], ((j + 1) >> 1) & 1);
-              if (!ok) break;
-              asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            }
-            score(x, j + 1);  // after the product that reads P_x, in issue order; its commit covers both
-            if (x == NX - 1) mma_commit(&k_empty[(j + 1) & 1]);
-          } else {
-            mma_commit(&o_done[x]);
+          if (ok) {
+            score(0, 0);
+            if constexpr (NX > 1) score(1, 0);
+            mma_commit(&k_empty[0]);
           }
         }
-      }
-      if (!ok) *failed = 1;
-      mma_commit(drained);  // nothing may be in flight when the columns are released
-      if (!bar_wait(drained, 0)) *failed = 1;
-    }
-  } else {
-    if constexpr (FMT == 0) {
-      // -------------------------------------------------------------- TMA producer
-      if (warp == 9 && lane == 0) {
-        int done = 0;
-        for (; done < nt; ++done) {
-          const int j = done, s = j & 1;
-          int pg[4];
-          uint32_t boxes = 0;
+        for (int j = 0; ok && j < nt; ++j) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int u = 4 * tile_at(j) + q;
-            pg[q] = u < pages ? cache_page(c, b, base_at(u) / kKvPage) : -1;
-            boxes += pg[q] >= 0 ? 1u : 0u;
-          }
-          if (j >= 2 && !bar_wait(&k_empty[s], ((j >> 1) - 1) & 1)) break;
-          Info* in = info(j);
+          for (int x = 0; x < NX; ++x) {
+            ok = ok && bar_wait(&p_full[x], j & 1) && (x || bar_wait(FMT ? &v_full[j & 1] : &v_clean[j & 1], (j >> 1) & 1));
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t vb = smem_u32(sv) + (j & 1) * C::kTile;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int bq = pg[q] >= 0 ? base_at(4 * tile_at(j) + q) : kNowhere;
-            in->base[q] = bq;
-            in->poison[q] = 0;
-            in->whole[q] = quarter_whole(bq);
-          }
-          auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* full) {
-            mbar_arrive_expect_tx(full, boxes * (kKvPage * D * 2));
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (pg[q] >= 0)
-                for (int x = 0; x < C::kBoxes; ++x)
-                  tma_box(smem_u32(dst) + x * 16384 + q * (kKvPage * 128), map, x * 64,
-                          (pg[q] * c.Hkv + hkv) * kKvPage, full);
-          };
-          load(&map_k, sk + s * C::kTile, &k_full[s]);
-          if (j >= 2 && !bar_wait(&v_empty[s], ((j >> 1) - 1) & 1)) {
-            bar_wait(&k_full[s], (j >> 1) & 1);
-            break;
-          }
-          load(&map_v, sv + s * C::kTile, &v_full[s]);
-        }
-        if (done < nt) *failed = 1;
-        // every copy has landed before the CTA leaves
-        for (int j = max(0, done - 2); j < done; ++j)
-          if (!bar_wait(&k_full[j & 1], (j >> 1) & 1) || !bar_wait(&v_full[j & 1], (j >> 1) & 1)) break;
-      } else if (warp >= 10) {
-        // ------------------------------------------------------------ V cleaners: in mixed tiles, rows that
-        // nobody sees or that are not finite become zeros before the product reads them
-        const int t = threadIdx.x - 320;
-        for (int j = 0; j < nt; ++j) {
-          if (!bar_wait_warp(&v_full[j & 1], (j >> 1) & 1)) break;
-          Info* in = info(j);
-          uint8_t* vt = sv + (j & 1) * C::kTile;
-          for (int r = t; r < 128; r += 64) {
-            const int q = r >> 5, bq = in->base[q], kp = bq + (r & 31);
-            if (in->whole[q]) continue;
-            const bool dead = bq == kNowhere || !(kp <= posmax && (kp >= lowmin || kp < sinks));
-            bool bad = false;
-            if (!dead) {
-#pragma unroll
-              for (int ch = 0; ch < D / 8; ++ch) {
-                const uint4 v = *chunk_at(vt, r, ch);
-                const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  bad |= (w4[i] & 0x7F80u) == 0x7F80u || (w4[i] & 0x7F800000u) == 0x7F800000u;
+            for (int kk = 0; kk < 8; ++kk)
+              mma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, desc_mn(vb + kk * 2048), C::kIdescO,
+                     (j > 0 || kk > 0) ? 1u : 0u);
+            if (x == NX - 1) mma_commit(&v_empty[j & 1]);
+            if (j + 1 < nt) {
+              if (!x) {
+                ok = bar_wait(&k_full[(j + 1) & 1], ((j + 1) >> 1) & 1);
+                if (!ok) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
               }
-              if (bad) atomicOr(&in->poison[q], 1u << (r & 31));
+              score(x, j + 1);  // after the product that reads P_x, in issue order; its commit covers both
+              if (x == NX - 1) mma_commit(&k_empty[(j + 1) & 1]);
+            } else {
+              mma_commit(&o_done[x]);
             }
-            if (dead || bad)
+          }
+        }
+        if (!ok) *failed = 1;
+        mma_commit(drained);  // nothing may be in flight when the columns are released
+        if (!bar_wait(drained, 0)) *failed = 1;
+      }
+    } else {
+      if constexpr (FMT == 0) {
+        // -------------------------------------------------------------- TMA producer
+        if (warp == 9 && lane == 0) {
+          int done = 0;
+          for (; done < nt; ++done) {
+            const int j = done, s = j & 1;
+            int pg[4];
+            uint32_t boxes = 0;
 #pragma unroll
-              for (int ch = 0; ch < D / 8; ++ch) *chunk_at(vt, r, ch) = make_uint4(0u, 0u, 0u, 0u);
+            for (int q = 0; q < 4; ++q) {
+              const int u = 4 * tile_at(j) + q;
+              pg[q] = u < pages ? cache_page(c, b, base_at(u) / kKvPage) : -1;
+              boxes += pg[q] >= 0 ? 1u : 0u;
+            }
+            if (j >= 2 && !bar_wait(&k_empty[s], ((j >> 1) - 1) & 1)) break;
+            Info* in = info(j);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int bq = pg[q] >= 0 ? base_at(4 * tile_at(j) + q) : kNowhere;
+              in->base[q] = bq;
+              in->poison[q] = 0;
+              in->whole[q] = quarter_whole(bq);
+            }
+            auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* full) {
+              mbar_arrive_expect_tx(full, boxes * (kKvPage * D * 2));
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                if (pg[q] >= 0)
+                  for (int x = 0; x < C::kBoxes; ++x)
+                    tma_box(smem_u32(dst) + x * 16384 + q * (kKvPage * 128), map, x * 64,
+                            (pg[q] * c.Hkv + hkv) * kKvPage, full);
+            };
+            load(&map_k, sk + s * C::kTile, &k_full[s]);
+            if (j >= 2 && !bar_wait(&v_empty[s], ((j >> 1) - 1) & 1)) {
+              bar_wait(&k_full[s], (j >> 1) & 1);
+              break;
+            }
+            load(&map_v, sv + s * C::kTile, &v_full[s]);
+          }
+          if (done < nt) *failed = 1;
+          // every copy has landed before the CTA leaves
+          for (int j = max(0, done - 2); j < done; ++j)
+            if (!bar_wait(&k_full[j & 1], (j >> 1) & 1) || !bar_wait(&v_full[j & 1], (j >> 1) & 1)) break;
+        } else if (warp >= 10) {
+          // ------------------------------------------------------------ V cleaners: in mixed tiles, rows that
+          // nobody sees or that are not finite become zeros before the product reads them
+          const int t = threadIdx.x - 320;
+          for (int j = 0; j < nt; ++j) {
+            if (!bar_wait_warp(&v_full[j & 1], (j >> 1) & 1)) break;
+            Info* in = info(j);
+            uint8_t* vt = sv + (j & 1) * C::kTile;
+            for (int r = t; r < 128; r += 64) {
+              const int q = r >> 5, bq = in->base[q], kp = bq + (r & 31);
+              if (in->whole[q]) continue;
+              const bool dead = bq == kNowhere || !(kp <= posmax && (kp >= lowmin || kp < sinks));
+              bool bad = false;
+              if (!dead) {
+#pragma unroll
+                for (int ch = 0; ch < D / 8; ++ch) {
+                  const uint4 v = *chunk_at(vt, r, ch);
+                  const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    bad |= (w4[i] & 0x7F80u) == 0x7F80u || (w4[i] & 0x7F800000u) == 0x7F800000u;
+                }
+                if (bad) atomicOr(&in->poison[q], 1u << (r & 31));
+              }
+              if (dead || bad)
+#pragma unroll
+                for (int ch = 0; ch < D / 8; ++ch) *chunk_at(vt, r, ch) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            mbar_arrive(&v_clean[j & 1]);
+          }
+        }
+      } else if (warp < 12) {
+        // -------------------------------------------------------------- converting warps, one page of a tile each
+        using L = Kv4<D>;
+        constexpr int NI = D / 32;     // 16-byte pieces of K (and of V) a lane takes
+        constexpr int PR = D / 32;     // pieces of a K row
+        const int w = warp - 8;
+        // V piece i of this lane: unit of (position pair column j, block, t); the order differs by t so that the
+        // lanes' rows fall into different banks
+        auto v_unit = [&](int i) {
+          if constexpr (D == 128) return ((i + lane) & 3) * 32 + lane;
+          return i * 32 + lane;
+        };
+        auto v_row = [&](int v) { return 8 * (v & 3) + 2 * (v / (D / 4)); };
+        // a piece's loads go out before the wait for its slot
+        uint4 raw[NI];
+        uint32_t ksb[NI], vsb[NI];
+        bool ok = true;
+        auto page_of = [&](int j) {  // of this warp's quarter of the j-th tile taken
+          const int u = 4 * tile_at(j) + w;
+          return j < nt && u < pages ? cache_page(c, b, base_at(u) / kKvPage) : -1;
+        };
+        int page = page_of(0);
+        for (int j = 0; j < nt; ++j) {
+          // (opaque to the compiler: kept across the loop, a lane's addresses would not fit its registers)
+          int ln = lane;
+          asm volatile("" : "+r"(ln));
+          const int s = j & 1;
+          const int base = page >= 0 ? base_at(4 * tile_at(j) + w) : kNowhere;
+          const uint8_t* kp = c.K + ((size_t)max(page, 0) * c.Hkv + hkv) * L::kBytes;
+          const uint8_t* vp = c.V + ((size_t)max(page, 0) * c.Hkv + hkv) * L::kBytes;
+          float krow = 0.f, vrow = 0.f;
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            const int e = i * 32 + lane, v = v_unit(i);  // K piece: row e / PR, elements 32 (e % PR) ..
+            raw[i] = make_uint4(0u, 0u, 0u, 0u);
+            ksb[i] = vsb[i] = 0;
+            if (page >= 0) {
+              raw[i] = __ldg(reinterpret_cast<const uint4*>(kp + e * 16));
+              ksb[i] = __ldg(reinterpret_cast<const uint16_t*>(kp + L::kCodes + e * 2));
+              vsb[i] = __ldg(reinterpret_cast<const uint16_t*>(vp + L::kCodes + (v % (D / 4)) / 4 * kKvPage + v_row(v)));
+            }
+          }
+          if (page >= 0) {
+            krow = __ldg(reinterpret_cast<const float*>(kp + L::kRows) + lane);
+            vrow = __ldg(reinterpret_cast<const float*>(vp + L::kRows) + lane);
+          }
+          // the next page's id, two loads ahead of its use
+          const int next = page_of(j + 1);
+          const int whole = quarter_whole(base);
+          uint32_t dead = 0, poison = 0;
+          if (!whole) {
+            const int pos = base + lane;
+            dead = __ballot_sync(0xFFFFFFFFu, !(pos <= posmax && (pos >= lowmin || pos < sinks)));
+            uint32_t bad = 0;
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+              bad |= (((vsb[i] & 0x7Fu) == 0x7Fu ? 1u : 0u) | ((vsb[i] & 0x7F00u) == 0x7F00u ? 2u : 0u))
+                     << v_row(v_unit(i));
+            poison = __reduce_or_sync(0xFFFFFFFFu, bad) & ~dead;
+          }
+          Info* in = info(j);
+          if (j >= 2 && !(ok = bar_wait_warp(&k_empty[s], ((j >> 1) - 1) & 1))) break;
+          if (lane == 0) {
+            in->base[w] = base;
+            in->poison[w] = poison;
+            in->whole[w] = whole;
+          }
+          in->ks[w * 32 + lane] = krow * p.scale_log2;
+          in->vs[w * 32 + lane] = (dead >> lane) & 1u ? 0.f : vrow;
+          // Row r = w * 32 + (32 i + lane) / PR, blocks 2 q and 2 q + 1 of it: chunk x of the four lies at the first one's
+          // address ^ x * 16 (r & 7 is the same for every i).  The lanes of a row's upper half store their blocks the
+          // other way round: no bank conflicts.
+          const int q = ln % PR, r0 = ln / PR;
+          const bool swap = (q >> 1) & 1;
+          const uint32_t kt = smem_u32(sk) + s * C::kTile + (q >> 1) * 16384 + (w * 32 + r0) * 128 +
+                              ((((4 * q) & 7) ^ (r0 & 7)) << 4);
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            const uint32_t words[4] = {swap ? raw[i].z : raw[i].x, swap ? raw[i].w : raw[i].y,
+                                       swap ? raw[i].x : raw[i].z, swap ? raw[i].y : raw[i].w};
+            const uint32_t s2 = e4m3x2_f16(swap ? __byte_perm(ksb[i], 0, 0x4401) : ksb[i]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint32_t h[4], o[4];
+              e2m1x8(words[x], h);
+              const uint32_t sd = __byte_perm(s2, 0, x < 2 ? 0x1010 : 0x3232);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const float2 f = scaled(h[y], sd);
+                o[y] = pack_bf16(f.x, f.y);
+              }
+              st_shared16((kt ^ ((x ^ (swap ? 2 : 0)) << 4)) + i * (32 / PR) * 128, o[0], o[1], o[2], o[3]);
+            }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          mbar_arrive(&v_clean[j & 1]);
-        }
-      }
-    } else if (warp < 12) {
-      // -------------------------------------------------------------- converting warps, one page of a tile each
-      using L = Kv4<D>;
-      constexpr int NI = D / 32;     // 16-byte pieces of K (and of V) a lane takes
-      constexpr int PR = D / 32;     // pieces of a K row
-      const int w = warp - 8;
-      // V piece i of this lane: unit of (position pair column j, block, t); the order differs by t so that the
-      // lanes' rows fall into different banks
-      auto v_unit = [&](int i) {
-        if constexpr (D == 128) return ((i + lane) & 3) * 32 + lane;
-        return i * 32 + lane;
-      };
-      auto v_row = [&](int v) { return 8 * (v & 3) + 2 * (v / (D / 4)); };
-      // a piece's loads go out before the wait for its slot
-      uint4 raw[NI];
-      uint32_t ksb[NI], vsb[NI];
-      bool ok = true;
-      auto page_of = [&](int j) {  // of this warp's quarter of the j-th tile taken
-        const int u = 4 * tile_at(j) + w;
-        return j < nt && u < pages ? cache_page(c, b, base_at(u) / kKvPage) : -1;
-      };
-      int page = page_of(0);
-      for (int j = 0; j < nt; ++j) {
-        // (opaque to the compiler: kept across the loop, a lane's addresses would not fit its registers)
-        int ln = lane;
-        asm volatile("" : "+r"(ln));
-        const int s = j & 1;
-        const int base = page >= 0 ? base_at(4 * tile_at(j) + w) : kNowhere;
-        const uint8_t* kp = c.K + ((size_t)max(page, 0) * c.Hkv + hkv) * L::kBytes;
-        const uint8_t* vp = c.V + ((size_t)max(page, 0) * c.Hkv + hkv) * L::kBytes;
-        float krow = 0.f, vrow = 0.f;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const int e = i * 32 + lane, v = v_unit(i);  // K piece: row e / PR, elements 32 (e % PR) ..
-          raw[i] = make_uint4(0u, 0u, 0u, 0u);
-          ksb[i] = vsb[i] = 0;
-          if (page >= 0) {
-            raw[i] = __ldg(reinterpret_cast<const uint4*>(kp + e * 16));
-            ksb[i] = __ldg(reinterpret_cast<const uint16_t*>(kp + L::kCodes + e * 2));
-            vsb[i] = __ldg(reinterpret_cast<const uint16_t*>(vp + L::kCodes + (v % (D / 4)) / 4 * kKvPage + v_row(v)));
-          }
-        }
-        if (page >= 0) {
-          krow = __ldg(reinterpret_cast<const float*>(kp + L::kRows) + lane);
-          vrow = __ldg(reinterpret_cast<const float*>(vp + L::kRows) + lane);
-        }
-        // the next page's id, two loads ahead of its use
-        const int next = page_of(j + 1);
-        const int whole = quarter_whole(base);
-        uint32_t dead = 0, poison = 0;
-        if (!whole) {
-          const int pos = base + lane;
-          dead = __ballot_sync(0xFFFFFFFFu, !(pos <= posmax && (pos >= lowmin || pos < sinks)));
-          uint32_t bad = 0;
+          mbar_arrive(&k_full[s]);
 #pragma unroll
           for (int i = 0; i < NI; ++i)
-            bad |= (((vsb[i] & 0x7Fu) == 0x7Fu ? 1u : 0u) | ((vsb[i] & 0x7F00u) == 0x7F00u ? 2u : 0u))
-                   << v_row(v_unit(i));
-          poison = __reduce_or_sync(0xFFFFFFFFu, bad) & ~dead;
-        }
-        Info* in = info(j);
-        if (j >= 2 && !(ok = bar_wait_warp(&k_empty[s], ((j >> 1) - 1) & 1))) break;
-        if (lane == 0) {
-          in->base[w] = base;
-          in->poison[w] = poison;
-          in->whole[w] = whole;
-        }
-        in->ks[w * 32 + lane] = krow * p.scale_log2;
-        in->vs[w * 32 + lane] = (dead >> lane) & 1u ? 0.f : vrow;
-        // Row r = w * 32 + (32 i + lane) / PR, blocks 2 q and 2 q + 1 of it: chunk x of the four lies at the first one's
-        // address ^ x * 16 (r & 7 is the same for every i).  The lanes of a row's upper half store their blocks the
-        // other way round: no bank conflicts.
-        const int q = ln % PR, r0 = ln / PR;
-        const bool swap = (q >> 1) & 1;
-        const uint32_t kt = smem_u32(sk) + s * C::kTile + (q >> 1) * 16384 + (w * 32 + r0) * 128 +
-                            ((((4 * q) & 7) ^ (r0 & 7)) << 4);
+            if (page >= 0) raw[i] = __ldg(reinterpret_cast<const uint4*>(vp + v_unit(i) * 16));
+          if (j >= 2 && !(ok = bar_wait_warp(&v_empty[s], ((j >> 1) - 1) & 1))) break;
+          dead |= poison;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const uint32_t words[4] = {swap ? raw[i].z : raw[i].x, swap ? raw[i].w : raw[i].y,
-                                     swap ? raw[i].x : raw[i].z, swap ? raw[i].y : raw[i].w};
-          const uint32_t s2 = e4m3x2_f16(swap ? __byte_perm(ksb[i], 0, 0x4401) : ksb[i]);
+          for (int i = 0; i < NI; ++i) {
+            // rows r and r + 1 (r even) of block blk: chunk h of row r at vt ^ h * 16, of row r + 1 at (vt + 128) ^ 16 ^ h * 16
+            const int v = D == 128 ? ((i + ln) & 3) * 32 + ln : i * 32 + ln;
+            const int r = v_row(v), blk = (v % (D / 4)) / 4;
+            const uint32_t vt = smem_u32(sv) + s * C::kTile + (blk >> 2) * 16384 + (w * 32 + r) * 128 +
+                                ((((2 * blk) & 7) ^ (r & 7)) << 4);
+            const uint32_t words[4] = {blk & 1 ? raw[i].z : raw[i].x, blk & 1 ? raw[i].w : raw[i].y,
+                                       blk & 1 ? raw[i].x : raw[i].z, blk & 1 ? raw[i].y : raw[i].w};
+            uint32_t sb = vsb[i];
+            if ((dead >> r) & 1u) sb &= 0xFF00u;
+            if ((dead >> r) & 2u) sb &= 0x00FFu;
+            const uint32_t s2 = e4m3x2_f16(sb);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t h[4], o[4];
-            e2m1x8(words[x], h);
-            const uint32_t sd = __byte_perm(s2, 0, x < 2 ? 0x1010 : 0x3232);
+            for (int x = 0; x < 4; x += 2) {
+              uint32_t h[4], g[4], o0[4], o1[4];
+              e2m1x8(words[x], h);
+              e2m1x8(words[x + 1], g);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const float2 f = scaled(h[y], sd);
-              o[y] = pack_bf16(f.x, f.y);
+              for (int y = 0; y < 2; ++y) {
+                const float2 f0 = scaled(h[2 * y], s2), f1 = scaled(h[2 * y + 1], s2);
+                const float2 g0 = scaled(g[2 * y], s2), g1 = scaled(g[2 * y + 1], s2);
+                o0[y] = pack_bf16(f0.x, f1.x);
+                o1[y] = pack_bf16(f0.y, f1.y);
+                o0[2 + y] = pack_bf16(g0.x, g1.x);
+                o1[2 + y] = pack_bf16(g0.y, g1.y);
+              }
+              const uint32_t h16 = (x / 2 ^ (blk & 1)) << 4;
+              st_shared16(vt ^ h16, o0[0], o0[1], o0[2], o0[3]);
+              st_shared16((vt + 128) ^ 16 ^ h16, o1[0], o1[1], o1[2], o1[3]);
             }
-            st_shared16((kt ^ ((x ^ (swap ? 2 : 0)) << 4)) + i * (32 / PR) * 128, o[0], o[1], o[2], o[3]);
           }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          mbar_arrive(&v_full[s]);
+          page = next;
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        mbar_arrive(&k_full[s]);
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-          if (page >= 0) raw[i] = __ldg(reinterpret_cast<const uint4*>(vp + v_unit(i) * 16));
-        if (j >= 2 && !(ok = bar_wait_warp(&v_empty[s], ((j >> 1) - 1) & 1))) break;
-        dead |= poison;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          // rows r and r + 1 (r even) of block blk: chunk h of row r at vt ^ h * 16, of row r + 1 at (vt + 128) ^ 16 ^ h * 16
-          const int v = D == 128 ? ((i + ln) & 3) * 32 + ln : i * 32 + ln;
-          const int r = v_row(v), blk = (v % (D / 4)) / 4;
-          const uint32_t vt = smem_u32(sv) + s * C::kTile + (blk >> 2) * 16384 + (w * 32 + r) * 128 +
-                              ((((2 * blk) & 7) ^ (r & 7)) << 4);
-          const uint32_t words[4] = {blk & 1 ? raw[i].z : raw[i].x, blk & 1 ? raw[i].w : raw[i].y,
-                                     blk & 1 ? raw[i].x : raw[i].z, blk & 1 ? raw[i].y : raw[i].w};
-          uint32_t sb = vsb[i];
-          if ((dead >> r) & 1u) sb &= 0xFF00u;
-          if ((dead >> r) & 2u) sb &= 0x00FFu;
-          const uint32_t s2 = e4m3x2_f16(sb);
-#pragma unroll
-          for (int x = 0; x < 4; x += 2) {
-            uint32_t h[4], g[4], o0[4], o1[4];
-            e2m1x8(words[x], h);
-            e2m1x8(words[x + 1], g);
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const float2 f0 = scaled(h[2 * y], s2), f1 = scaled(h[2 * y + 1], s2);
-              const float2 g0 = scaled(g[2 * y], s2), g1 = scaled(g[2 * y + 1], s2);
-              o0[y] = pack_bf16(f0.x, f1.x);
-              o1[y] = pack_bf16(f0.y, f1.y);
-              o0[2 + y] = pack_bf16(g0.x, g1.x);
-              o1[2 + y] = pack_bf16(g0.y, g1.y);
-            }
-            const uint32_t h16 = (x / 2 ^ (blk & 1)) << 4;
-            st_shared16(vt ^ h16, o0[0], o0[1], o0[2], o0[3]);
-            st_shared16((vt + 128) ^ 16 ^ h16, o1[0], o1[1], o1[2], o1[3]);
-          }
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        mbar_arrive(&v_full[s]);
-        page = next;
+        if (!ok && lane == 0) *failed = 1;
       }
-      if (!ok && lane == 0) *failed = 1;
     }
-  }
   } else {
     if constexpr (FMT == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     // ---------------------------------------------------------------- softmax: a warp has 32 pairs (its TMEM
@@ -680,16 +720,43 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
         if (FMT == 0 && !(ok = bar_wait_warp(&v_clean[j & 1], (j >> 1) & 1))) break;
         kind = (in->poison[0] | in->poison[1] | in->poison[2] | in->poison[3]) ? 2 : 1;
       }
-      // One pass relative to the maximum of the tiles before, p packed in registers.  On a row's first tile, or
-      // when a sum comes out too large, the scores (still in TMEM) give a new maximum, O is rescaled and the pass
-      // taken (again).
-      uint32_t pk[4][2][8];  // [32 keys][16 pairs][register of the store]
-      float sum[4];
       auto masks = [&](int q, uint32_t (&see)[4]) {  // bits 8 i + e: columns 8 i + 2 t + e of the quarter
 #pragma unroll
         for (int k = 0; k < 4; ++k) see[k] = sees(in->base[q], pos[k], low[k], sinks) >> (2 * lt);
       };
-      auto pass = [&](auto w_) {
+      auto load = [&](int q, uint32_t (&s)[2][16]) {
+        tm_frag_ld(t_s + q * 32, s[0]);
+        tm_frag_ld(t_s + (16u << 16) + q * 32, s[1]);
+      };
+      // The largest log2 weight (relative to `ref`, or absolute) that each of the lane's rows sees in a quarter.
+      auto top_of = [&](int q, bool relative, float (&mx)[4]) {
+        uint32_t s[2][16], see[4];
+        load(q, s);
+        masks(q, see);
+        tm_wait_ld(s);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float2 ks = make_float2(p.scale_log2, p.scale_log2);
+          if constexpr (FMT == 1) ks = *reinterpret_cast<const float2*>(in->ks + q * 32 + 8 * i + 2 * lt);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t* sr = &s[k >> 1][4 * i + 2 * (k & 1)];
+            if ((see[k] >> (8 * i)) & 1u) mx[k] = fmaxf(mx[k], __uint_as_float(sr[0]) * ks.x);
+            if ((see[k] >> (8 * i)) & 2u) mx[k] = fmaxf(mx[k], __uint_as_float(sr[1]) * ks.y);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xFFFFFFFFu, mx[k], 1));
+          mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xFFFFFFFFu, mx[k], 2));
+          if (relative) mx[k] -= ref[k];
+        }
+      };
+      // C::kGroup quarters of the tile from q0 on: p relative to ref, their sums, and p (times V's row scale) packed for
+      // the store.
+      auto group = [&](auto w_, int q0, float (&sum)[4], uint32_t (&pk)[C::kGroup][2][8]) {
         constexpr int kKind = decltype(w_)::value;
         uint64_t nm2[4], sum2[4];
 #pragma unroll
@@ -699,32 +766,30 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
           sum2[k] = 0;
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t s[2][16];
-          tm_frag_ld(t_s + q * 32, s[0]);
-          tm_frag_ld(t_s + (16u << 16) + q * 32, s[1]);
-          float2 ks[FMT ? 4 : 1], vs[FMT ? 4 : 1];
-          if constexpr (FMT == 1) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              ks[i] = *reinterpret_cast<const float2*>(in->ks + q * 32 + 8 * i + 2 * lt);
-              vs[i] = *reinterpret_cast<const float2*>(in->vs + q * 32 + 8 * i + 2 * lt);
-            }
-          }
-          uint32_t see[4], poison = 0;
-          if constexpr (kKind > 0) {
-            masks(q, see);
-            if constexpr (kKind == 2) poison = in->poison[q] >> (2 * lt);
-          }
-          tm_wait_ld();
+        for (int h = 0; h < C::kGroup; ++h) {
+          const int q = q0 + h;
+          uint32_t s[2][16], see[4], poison = 0;
+          load(q, s);
+          if constexpr (kKind > 0) masks(q, see);
+          if constexpr (kKind == 2) poison = in->poison[q] >> (2 * lt);
+          float2 kss[4], vss[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint64_t ks2 = FMT ? pair2(ks[FMT ? i : 0].x, ks[FMT ? i : 0].y) : pair2(p.scale_log2, p.scale_log2);
+            kss[i] = vss[i] = make_float2(p.scale_log2, p.scale_log2);
+            if constexpr (FMT == 1) {
+              kss[i] = *reinterpret_cast<const float2*>(in->ks + q * 32 + 8 * i + 2 * lt);
+              vss[i] = *reinterpret_cast<const float2*>(in->vs + q * 32 + 8 * i + 2 * lt);
+            }
+          }
+          tm_wait_ld(s);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 ks = kss[i], vs = vss[i];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t* sr = &s[k >> 1][4 * i + 2 * (k & 1)];
               float t0, t1;
-              unpair2(fma2(pair2(__uint_as_float(sr[0]), __uint_as_float(sr[1])), ks2, nm2[k]), t0, t1);
+              unpair2(fma2(pair2(__uint_as_float(sr[0]), __uint_as_float(sr[1])), pair2(ks.x, ks.y), nm2[k]), t0, t1);
               t0 = ex2f(t0);
               t1 = ex2f(t1);
               if constexpr (kKind > 0) {
@@ -738,13 +803,13 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
               const uint64_t t2 = pair2(t0, t1);
               sum2[k] = add2(sum2[k], t2);
               if constexpr (FMT == 1) {
-                unpair2(mul2(t2, pair2(vs[FMT ? i : 0].x, vs[FMT ? i : 0].y)), t0, t1);
+                unpair2(mul2(t2, pair2(vs.x, vs.y)), t0, t1);
                 if constexpr (kKind > 0) {  // an unseen row's scale may be anything
                   t0 = (see[k] >> (8 * i)) & 1u ? t0 : 0.f;
                   t1 = (see[k] >> (8 * i)) & 2u ? t1 : 0.f;
                 }
               }
-              pk[q][k >> 1][2 * i + (k & 1)] = pack_bf16(t0, t1);
+              pk[h][k >> 1][2 * i + (k & 1)] = pack_bf16(t0, t1);
             }
           }
         }
@@ -755,52 +820,58 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
           sum[k] = a + b2;
         }
       };
-      bool again = false;
+      // To begin with, any reference near the maximum does: that of the first quarters in which every row of the
+      // warp sees a key.
+      bool none = false;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) again |= ref[k] == -INFINITY;
-      again = __any_sync(0xFFFFFFFFu, again);
-      for (int round = 0; round < 2; ++round) {
-        if (again) {
-          float mx[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mx[k] = -INFINITY;
+      for (int k = 0; k < 4; ++k) none |= ref[k] == -INFINITY;
+      if (__any_sync(0xFFFFFFFFu, none)) {
 #pragma unroll 1
-          for (int q = 3; q >= 0; --q) {
-            uint32_t s[2][16], see[4];
-            tm_frag_ld(t_s + q * 32, s[0]);
-            tm_frag_ld(t_s + (16u << 16) + q * 32, s[1]);
-            masks(q, see);
-            tm_wait_ld();
+        for (int q = 3; q >= 0; --q) {
+          float mx[4];
+          top_of(q, false, mx);
+          none = false;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float2 ks = make_float2(p.scale_log2, p.scale_log2);
-              if constexpr (FMT == 1) ks = *reinterpret_cast<const float2*>(in->ks + q * 32 + 8 * i + 2 * lt);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t* sr = &s[k >> 1][4 * i + 2 * (k & 1)];
-                if ((see[k] >> (8 * i)) & 1u) mx[k] = fmaxf(mx[k], __uint_as_float(sr[0]) * ks.x);
-                if ((see[k] >> (8 * i)) & 2u) mx[k] = fmaxf(mx[k], __uint_as_float(sr[1]) * ks.y);
-              }
-            }
-            // to begin with any reference near the maximum does: the keys of one quarter, if every row sees some
-            if (round == 0) {
-              bool none = false;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) none |= mx[k] == -INFINITY;
-              if (!__any_sync(0xFFFFFFFFu, none)) break;
-            }
+          for (int k = 0; k < 4; ++k) {  // (a row that has a reference keeps it; one without has only zeros so far)
+            if (ref[k] == -INFINITY) ref[k] = mx[k];
+            none |= ref[k] == -INFINITY;
           }
-          float alpha[4];
+          if (!__any_sync(0xFFFFFFFFu, none)) break;
+        }
+      }
+      // The p of a group go over the scores of the tile's first half as 16 columns a quarter: over scores that are
+      // done, so that the group can be taken again.
+#pragma unroll
+      for (int q = 0; q < 4; q += C::kGroup) {
+        uint32_t pk[C::kGroup][2][8];  // [32 keys][16 pairs][register of the store]
+        float sum[4];
+        auto compute = [&]() {
+          if (kind == 0)
+            group(std::integral_constant<int, 0>{}, q, sum, pk);
+          else if (kind == 1)
+            group(std::integral_constant<int, 1>{}, q, sum, pk);
+          else
+            group(std::integral_constant<int, 2>{}, q, sum, pk);
+        };
+        compute();
+        const bool much = sum[0] > kMaxSum || sum[1] > kMaxSum || sum[2] > kMaxSum || sum[3] > kMaxSum;
+        if (__any_sync(0xFFFFFFFFu, much)) {
+          // Replace the references by a power of two, so that everything so far (sums, outputs, p of the quarters
+          // before, which are in TMEM) is rescaled exactly, and take the group again.
+          float mx[4], alpha[4];
+          top_of(q, true, mx);
+#pragma unroll 1
+          for (int h = 1; h < C::kGroup; ++h) {
+            float m2[4];
+            top_of(q + h, true, m2);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], m2[k]);
+          }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            float m = mx[k];
-            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-            alpha[k] = 1.f;
-            if (m > ref[k]) {
-              if (ref[k] != -INFINITY) alpha[k] = ex2f(ref[k] - m);
-              ref[k] = m;
-            }
+            const float up = fmaxf(ceilf(mx[k]), 0.f);
+            alpha[k] = ex2f(-up);
+            ref[k] += up;
             l[k] *= alpha[k];
           }
           if (j > 0) {  // the product with the previous tile is done (s_full)
@@ -810,29 +881,35 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
               const float a0 = d >= D ? alpha[2] : alpha[0], a1 = d >= D ? alpha[3] : alpha[1];
               uint32_t r[16];
               tm_frag_ld(at, r);
-              tm_wait_ld();
+              tm_wait_ld(r);
 #pragma unroll
               for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * (i & 2 ? a1 : a0));
               tm_frag_st(at, r);
             }
           }
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+#pragma unroll 1
+          for (int e = 0; e < 2 * q; ++e) {
+            const uint32_t at = t_s + (e & 1 ? 16u << 16 : 0u) + (e >> 1) * 16;
+            uint32_t r[8];
+            tm_pair_ld(at, r);
+            tm_wait_ld(r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float a = e & 1 ? (i & 1 ? alpha[3] : alpha[2]) : (i & 1 ? alpha[1] : alpha[0]);
+              r[i] = pack_bf16(bf16_lo(r[i]) * a, bf16_hi(r[i]) * a);
+            }
+            tm_pair_st(at, r);
+          }
+          compute();
         }
-        if (kind == 0)
-          pass(std::integral_constant<int, 0>{});
-        else if (kind == 1)
-          pass(std::integral_constant<int, 1>{});
-        else
-          pass(std::integral_constant<int, 2>{});
-        again = sum[0] > kMaxSum || sum[1] > kMaxSum || sum[2] > kMaxSum || sum[3] > kMaxSum;
-        if (!__any_sync(0xFFFFFFFFu, again)) break;
-        again = true;
-      }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) l[k] += sum[k];
+        for (int k = 0; k < 4; ++k) l[k] += sum[k];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        tm_pair_st(t_s + q * 16, pk[q][0]);
-        tm_pair_st(t_s + (16u << 16) + q * 16, pk[q][1]);
+        for (int h = 0; h < C::kGroup; ++h) {
+          tm_pair_st(t_s + (q + h) * 16, pk[h][0]);
+          tm_pair_st(t_s + (16u << 16) + (q + h) * 16, pk[h][1]);
+        }
       }
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -885,26 +962,26 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
           asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // (shared memory is read, then the CTA may end)
         }
       } else {
-      __syncwarp();
-      const int64_t at = pair_at(col0 + lane, p.out_stride);
+        __syncwarp();
+        const int64_t at = pair_at(col0 + lane, p.out_stride);
 #pragma unroll 4
-      for (int it = 0; it < kChunks; ++it) {
-        const int r = it * kLines + lane / kChunks, ch = lane % kChunks;
-        const uint4 v = *chunk_at(rows, r0 + r, ch);
-        uint16_t* dst = static_cast<uint16_t*>(p.out) + from_lane(at, r) + ch * 8;
-        if (col0 + r < ncol) {
-          if ((reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
-            *reinterpret_cast<uint4*>(dst) = v;
-          } else {
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int it = 0; it < kChunks; ++it) {
+          const int r = it * kLines + lane / kChunks, ch = lane % kChunks;
+          const uint4 v = *chunk_at(rows, r0 + r, ch);
+          uint16_t* dst = static_cast<uint16_t*>(p.out) + from_lane(at, r) + ch * 8;
+          if (col0 + r < ncol) {
+            if ((reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
+              *reinterpret_cast<uint4*>(dst) = v;
+            } else {
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              dst[2 * i] = static_cast<uint16_t>(w[i]);
-              dst[2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
+              for (int i = 0; i < 4; ++i) {
+                dst[2 * i] = static_cast<uint16_t>(w[i]);
+                dst[2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
+              }
             }
           }
         }
-      }
       }
     } else if (!ok && lane == 0) {
       *failed = 1;

@@ -172,6 +172,32 @@ def test_rows_of_very_different_sizes(fmt, counts):
             check(batch, q, attend(batch, q, 4, dtype), 4, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("counts", [[1], [9], [200]])
+@pytest.mark.parametrize("what", ["ramp", "jump", "values"])
+def test_references_that_have_to_be_replaced(fmt, dtype, counts, what):
+    """Scores that grow with the position (every reference is soon too small), one that jumps by 2^200 over the rest,
+    and values whose size grows by 2^40 while the scores fall."""
+    n = 700
+    pool = Pool(fmt, 1, 128, [n], seed=4)
+    rng = np.random.default_rng(1)
+    d = rng.choice(np.array([-1.0, 1.0], np.float32), 128)
+    top = np.linspace(0, 60, n) if what == "ramp" else np.linspace(0, 3, n)      # scores, natural logarithm
+    if what == "jump":
+        top[[333, 520]] = 140
+    if what == "values":
+        top = np.linspace(25, 0, n)
+        v = rng.standard_normal((n, 1, 128)) * 2.0 ** np.linspace(-20, 20, n)[:, None, None]
+        pool.v[0][:] = pool.put(1, 0, 0, v.astype(np.float32))
+    k = d * top[:, None].astype(np.float32) * np.float32(128 ** 0.5 / 128) + 0.05 * rng.standard_normal((n, 128))
+    pool.k[0][:] = pool.put(0, 0, 0, k.astype(np.float32)[:, None])
+    batch = Batch(pool, counts)
+    q = torch.from_numpy(np.tile(d, (batch.n_rows, 4)).astype(np.float32)).to(TYPES[dtype]).to(DEV)
+    check(batch, q, attend(batch, q, 4, dtype), 4, dtype)
+    check(batch, q, attend(batch, q, 4, dtype, 450, 7), 4, dtype, 450, 7)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_constant_values_come_back(fmt):
     """softmax weights sum to one: values that are the same everywhere are the result."""
