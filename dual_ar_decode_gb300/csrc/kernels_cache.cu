@@ -84,46 +84,62 @@ __device__ __forceinline__ void store_row(void* base, size_t off, int f32, const
   }
 }
 
-// Two floats -> two e2m1 codes in a byte (the first in the low nibble): round to nearest even, +-6 at most.
-__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
-  uint16_t d;
-  asm("{.reg .b8 b; cvt.rn.satfinite.e2m1x2.f32 b, %1, %2; mov.b16 %0, {b, 0};}" : "=h"(d) : "f"(hi), "f"(lo));
+// Eight floats -> eight e2m1 codes (the first in the lowest nibble): round to nearest even, +-6 at most.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&r)[8]) {
+  uint32_t d;
+  asm("{.reg .b8 b0, b1, b2, b3;"
+      " cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1; cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;"
+      " cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5; cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;"
+      " mov.b32 %0, {b0, b1, b2, b3};}"
+      : "=r"(d)
+      : "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]));
+  return d;
+}
+__device__ __forceinline__ float max_abs_nan(float a, float x) {  // a NaN if x is one
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(fabsf(x)));
   return d;
 }
 
-// x: one block of a row, LANES lanes hold the row.  Its codes (two per byte), its scale byte, the row's scale.
+// x: one block of a row, LANES lanes hold the row.  Its codes (the first element in the lowest nibble), its scale
+// byte, the row's scale.
 template <int LANES>
-__device__ __forceinline__ void quantise_row(const float (&x)[16], uint32_t (&code)[8], uint32_t& sb, float& s) {
-  uint32_t blk = 0;  // |x| as bits: ordered like the values, infinities and NaN above them
+__device__ __forceinline__ void quantise_row(const float (&x)[16], uint32_t (&code)[2], uint32_t& sb, float& s) {
+  float blk = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) blk = max(blk, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-  uint32_t row = blk;
+  for (int i = 0; i < 16; ++i) blk = max_abs_nan(blk, x[i]);
+  float row = blk;
 #pragma unroll
-  for (int o = 1; o < LANES; o <<= 1) row = max(row, __shfl_xor_sync(0xFFFFFFFFu, row, o));
-  s = row >= 0x7F800000u ? __int_as_float(0x7FFFFFFF) : __fdiv_rn(__uint_as_float(row), 2688.0f);
+  for (int o = 1; o < LANES; o <<= 1) row = max_abs_nan(row, __shfl_xor_sync(0xFFFFFFFFu, row, o));
+  s = row < INFINITY ? __fdiv_rn(row, 2688.0f) : __int_as_float(0x7FFFFFFF);
   const float s6 = __fmul_rn(s, 6.0f);
   sb = 0;
   float step = 0.f;
   if (s6 > 0.f) {  // false for NaN
-    sb = __nv_cvt_float_to_fp8(fminf(__fdiv_rn(__uint_as_float(blk), s6), 448.0f), __NV_SATFINITE, __NV_E4M3);
+    sb = __nv_cvt_float_to_fp8(fminf(__fdiv_rn(blk, s6), 448.0f), __NV_SATFINITE, __NV_E4M3);
     step = __fmul_rn(e4m3_value(sb), s);
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) code[i] = 0;
+  code[0] = code[1] = 0;
   if (!(step > 0.f)) return;
-  // The code is that of the rounded quotient x / step.  x * (1 / step) is within 2^-21 of it (two roundings and
-  // the reciprocal's); where both ends of that interval have the same code, it is the quotient's (rounding is
-  // monotonic), and only the few others need the division.
-  const float inv = __fdiv_rn(1.0f, step);
-  const bool safe = step > 1e-30f && step < 1e30f;
+  // The code is that of the rounded quotient x / step.  x * (1 / step) is within 2^-22 of it (the roundings of the
+  // reciprocal, of its scaling below and of the product, 2^-24 each), so the quotient lies between x * (1 / step) *
+  // (1 -+ 2^-21).  Where both have the same code, it is the quotient's (rounding is monotonic); only a block with
+  // others needs the divisions.
+  const float inv = __fdiv_rn(1.0f, step), down = inv * (1.0f - 4.76837158e-7f), up = inv * (1.0f + 4.76837158e-7f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float a = x[2 * i] * inv, b = x[2 * i + 1] * inv;
-    constexpr float kUp = 1.0f + 4.76837158e-7f, kDown = 1.0f - 4.76837158e-7f;
-    const uint32_t c0 = e2m1x2(a * kDown + 0.f, b * kDown + 0.f), c1 = e2m1x2(a * kUp + 0.f, b * kUp + 0.f);
-    code[i] = c0;
-    if (c0 != c1 || !safe)
-      code[i] = e2m1x2(__fdiv_rn(x[2 * i], step) + 0.f, __fdiv_rn(x[2 * i + 1], step) + 0.f);  // + 0: no -0
+  for (int h = 0; h < 2; ++h) {
+    float lo[8], hi[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // + 0: no -0
+      lo[i] = fmaf(x[8 * h + i], down, 0.f);
+      hi[i] = fmaf(x[8 * h + i], up, 0.f);
+    }
+    code[h] = e2m1x8(lo);
+    if (code[h] != e2m1x8(hi) || !(step > 1e-30f && step < 1e30f)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) lo[i] = __fdiv_rn(x[8 * h + i], step) + 0.f;
+      code[h] = e2m1x8(lo);
+    }
   }
 }
 
@@ -162,7 +178,7 @@ __global__ void __launch_bounds__(kRowThreads) k_cache_append(const CacheRowsPar
       dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
   } else {
-    uint32_t code[8], sb;
+    uint32_t code[2], sb;
     float s;
     quantise_row<LANES>(x, code, sb, s);
     if (mine) {
@@ -171,9 +187,7 @@ __global__ void __launch_bounds__(kRowThreads) k_cache_append(const CacheRowsPar
     }
     if (!isv) {
       if (mine)
-        *reinterpret_cast<uint2*>(head + r * (D / 2) + l * 8) =
-            make_uint2(code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24,
-                       code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24);
+        *reinterpret_cast<uint2*>(head + r * (D / 2) + l * 8) = make_uint2(code[0], code[1]);
     } else {
       // the even position's lane writes the pair's bytes; a position that this
       // call does not write keeps its nibble
@@ -182,8 +196,8 @@ __global__ void __launch_bounds__(kRowThreads) k_cache_append(const CacheRowsPar
       uint32_t out[4];
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const uint32_t two = code[2 * w] | code[2 * w + 1] << 16;      // elements 0, 1 and 2, 3: a nibble each
-        out[w] = (two & 0x000F000Fu) | (two & 0x00F000F0u) << 4;       // ... a byte each
+        const uint32_t two = __byte_perm(code[w >> 1], 0, w & 1 ? 0x4342 : 0x4140);  // elements 4 w .. + 3: a nibble each
+        out[w] = (two & 0x000F000Fu) | (two & 0x00F000F0u) << 4;                      // ... a byte each
         const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, out[w], LANES);
         if (both) {
           out[w] |= o << 4;
