@@ -16,9 +16,9 @@ namespace {
 
 // ---------------------------------------------------------------- rows in and out
 // Append: a lane takes one block of 16 elements of a row (D / 16 lanes a row), so a block's and a row's scale are
-// worked out with few idle repeats: the quantiser's divisions, not memory, bound it (16 x 512 rows of 8 heads,
-// bf16: 27 us with 8 elements a lane).  Even and odd position of a pair sit in one warp: a byte of V's codes holds
-// both, and one lane writes it.
+// worked out with few idle repeats: instructions (the quantiser's divisions), not memory, bound it.  16 x 512 bf16
+// rows of 8 heads: 16.5 us, 44 MB at 2.6 TB/s (27 us with 8 elements a lane); 394 instructions for 4 rows of a head.
+// Even and odd position of a pair sit in one warp: a byte of V's codes holds both, and one lane writes it.
 constexpr int kRowThreads = 128, kReadThreads = 256;
 
 template <int E>
@@ -223,7 +223,8 @@ __device__ __forceinline__ void e2m1x8_f16(uint32_t v, __half2 (&h)[4]) {
 }
 
 // Grid: (position pairs of a sequence * KV heads / 16, 2 (K, V), sequences): half a warp takes a pair of positions
-// of one head, E elements of both a lane, so V's codes (two positions in a byte) are read once.
+// of one head, E elements of both a lane, so V's codes (two positions in a byte) are read once.  16 x 512 rows of 8
+// heads to float32: 18 us, 77 MB at 4.3 TB/s, bound by the writes.
 template <int D, int FMT>
 __global__ void __launch_bounds__(kReadThreads) k_cache_read(const CacheRowsParams p) {
   constexpr int E = D / 16;
@@ -297,7 +298,8 @@ __global__ void __launch_bounds__(kReadThreads) k_cache_read(const CacheRowsPara
 }
 
 // ---------------------------------------------------------------- page copies
-// The lists travel as kernel parameters, so a call needs no device staging.
+// The lists travel as kernel parameters, so a call needs no device staging.  64 pages of 64 KB in 72 pools: 88.6 us,
+// 6.8 TB/s; one page of 19 KB in 72 pools: 1.8 us.
 constexpr int kCopyPools = 128, kCopyMoves = 384;
 struct CopyParams {
   uint4* pool[kCopyPools];

@@ -27,6 +27,11 @@
 //     sees are zeroed in shared memory (0 x NaN is NaN); a V row with an infinity
 //     or a NaN that only some rows see is zeroed too and made a NaN probability
 //     of the rows that see it.
+// Measured (GB300, 32 query and 8 KV heads of 128): a tile of 128 keys takes a CTA
+// about 3200 cycles with bf16 pages (the four products; 2600 at the measured dense
+// rate) and 5000 with 4-bit pages (the softmax behind the products: its scales and
+// the converters' instructions).  Four ragged chunks of up to 1024 rows, window 1024:
+// 73 us (53 GFLOP); 2 x 1024 rows over 5120 4-bit positions: 200 us (155 GFLOP).
 // Every wait is bounded; the TMEM columns are always released.
 #include <cuda.h>
 #include <cuda_fp16.h>

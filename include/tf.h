@@ -532,9 +532,13 @@ int64_t tf_op_cache_page_bytes(int32_t format, int32_t n_kv_heads, int32_t head_
  * apart (0: n_heads*D), of type `dtype` (TF_DTYPE_F32 or TF_DTYPE_BF16); query
  * head h reads KV head h / (n_heads / n_kv_heads), a ratio of 1 to 8.  out must
  * not overlap q or the pools.  scale > 0 (0: 1/sqrt(D)).
+ * A row that does see a position with an infinity or a NaN may become NaN in
+ * all its elements.
  * Scores, softmax statistics and sums are float32; with TF_DTYPE_F32 queries
  * and probabilities enter the matrix products with 22 or more significant
  * bits, with TF_DTYPE_BF16 the probabilities enter as bfloat16 or float16.
+ * (4-bit pages: a probability times its V row's scale keeps these bits down to
+ * 2^-32 of the largest such product.)
  * Errors: TF_E_INVAL, TF_E_CUDA. */
 tf_status tf_op_attention_cache(const tf_kv_cache* cache, const void* q, int64_t q_stride, void* out,
                                 int64_t out_stride, int32_t dtype, int32_t n_heads, int32_t window,
