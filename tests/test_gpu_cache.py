@@ -417,3 +417,147 @@ def test_captured_calls_read_lengths_when_they_run(fmt, counts):
                            stream=streams[i % 3].cuda_stream)
     torch.cuda.synchronize()
     assert all(torch.equal(o, out) for o in outs)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("window,sinks", [(1, 0), (20, 10 ** 6), (33, 33), (64, 31), (500, 1)])
+def test_windows_over_prompt_rows(fmt, dtype, window, sinks):
+    """Windows narrower than the rows of a call, sinks that reach into them, windows that begin inside a page."""
+    lens, counts = [300, 40, 613], [290, 40, 77]
+    batch = Batch(Pool(fmt, 1, 64, lens, seed=window), counts)
+    q = queries(batch, 4, dtype, 2)
+    check(batch, q, attend(batch, q, 4, dtype, window, sinks), 4, dtype, window, sinks)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_more_sequences_than_a_cta_sorts(fmt):
+    lens = [(i * 37) % 70 for i in range(400)]
+    batch = Batch(Pool(fmt, 1, 64, lens, seed=5), [1] * 400)
+    for dtype in ("f32", "bf16"):
+        q = queries(batch, 2, dtype, 2)
+        check(batch, q, attend(batch, q, 2, dtype), 2, dtype)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("counts", [[1, 1, 1], [60, 50, 40]])
+def test_sequences_that_share_pages(fmt, counts):
+    """A common past: the block tables name the same pages, one of them twice in a row of the table."""
+    pool = Pool(fmt, 2, 64, [100, 100, 96], seed=5)
+    pool.table[1, :3] = pool.table[0, :3]
+    pool.table[2, :3] = pool.table[0, [0, 0, 1]]
+    pos = [np.arange(100), np.concatenate((np.arange(96), np.arange(96, 100))),
+           np.concatenate((np.arange(32), np.arange(32), np.arange(32, 64)))]
+    k, v = pool.k[0].copy(), pool.v[0].copy()
+    own_k, own_v = pool.k[1].copy(), pool.v[1].copy()
+    pool.k[2], pool.v[2] = k[pos[2]], v[pos[2]]
+    pool.k[1] = np.concatenate((k[:96], own_k[96:]))
+    pool.v[1] = np.concatenate((v[:96], own_v[96:]))
+    batch = Batch(pool, counts)
+    for dtype in ("f32", "bf16"):
+        q = queries(batch, 8, dtype, 2)
+        check(batch, q, attend(batch, q, 8, dtype), 8, dtype)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_pools_beyond_four_gigabytes(fmt):
+    """Pages whose byte offset passes 32 bits: attention (both kernels), append, read and copy."""
+    Hkv, D = 8, 128
+    page = cache_page_bytes(fmt, Hkv, D)
+    n_pages = (5 << 30) // page
+    small = Pool(fmt, Hkv, D, [70], seed=3, spare=0)
+    at = np.array([n_pages - 1, n_pages // 2 + 7, n_pages - 3], np.int32)
+    K = torch.empty((n_pages, page), dtype=torch.uint8, device=DEV)
+    V = torch.empty_like(K)
+    for pool, src in ((K, small.K), (V, small.V)):
+        pool[torch.from_numpy(at).long().to(DEV)] = torch.from_numpy(
+            src[small.table[0]].reshape(3, page)).to(DEV)
+    table = torch.from_numpy(at).to(DEV)
+    for r in (1, 65):
+        lens = torch.tensor([70], dtype=torch.int32, device=DEV)
+        start = torch.tensor([0, r], dtype=torch.int32, device=DEV)
+        cache = kv_cache(fmt, Hkv, D, K.data_ptr(), V.data_ptr(), n_pages, table.data_ptr(), 3, 1, lens.data_ptr(),
+                         start.data_ptr(), r, r)
+        for dtype in ("f32", "bf16"):
+            q = torch.randn((r, 32 * D), device=DEV).to(TYPES[dtype])
+            out = torch.empty_like(q)
+            op_attention_cache(cache, q.data_ptr(), out.data_ptr(), dtype, 32)
+            qn = q.float().cpu().numpy().astype(np.float64).reshape(r, 32, D)
+            want, *sizes = attention(qn, small.k[0], small.v[0], 70)
+            tol = tolerance(want, *sizes, D, 70, dtype, fmt)
+            assert np.all(np.abs(out.float().cpu().numpy().reshape(r, 32, D) - want) <= tol)
+    got = torch.empty((2, 65, Hkv, D), device=DEV)
+    op_cache_read(cache, got[0].data_ptr(), got[1].data_ptr(), "f32")
+    assert np.array_equal(got[0].cpu().numpy(), small.k[0][5:].astype(np.float32))
+    assert np.array_equal(got[1].cpu().numpy(), small.v[0][5:].astype(np.float32))
+    x = torch.randn((65, Hkv * D), device=DEV)
+    op_cache_append(cache, x.data_ptr(), x.data_ptr(), "f32")
+    op_cache_read(cache, got[0].data_ptr(), got[1].data_ptr(), "f32")
+    assert torch.equal(got[0], got[1]) and not torch.equal(got[0], torch.zeros_like(got[0]))
+    op_cache_copy([K.data_ptr(), V.data_ptr()], page, n_pages, at[:1], [n_pages - 2])
+    assert torch.equal(K[n_pages - 2], K[n_pages - 1]) and torch.equal(V[n_pages - 2], V[n_pages - 1])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_decode_step_captured_whole(fmt):
+    """append, attention, read and a page copy in one graph, replayed with other rows and lengths; no err word, no
+    row_start."""
+    pool = Pool(fmt, 2, 64, [70, 33, 64], seed=5, spare=4)
+    batch = Batch(pool, [1, 1, 1])
+    batch.cache.row_start = None
+    batch.cache.err = None
+    k, v = torch.zeros((3, 128), device=DEV), torch.zeros((3, 128), device=DEV)
+    back = torch.zeros((2, 3, 128), dtype=torch.bfloat16, device=DEV)
+    q = queries(batch, 8, "f32", 1)
+    out = torch.zeros_like(q)
+    free = sorted(set(range(pool.n_pages)) - set(pool.table[pool.table >= 0].tolist()))[0]
+    src = int(pool.table[0, 0])
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=side):
+        s = torch.cuda.current_stream().cuda_stream
+        op_cache_append(batch.cache, k.data_ptr(), v.data_ptr(), "f32", s)
+        op_attention_cache(batch.cache, q.data_ptr(), out.data_ptr(), "f32", 8, 40, 3, stream=s)
+        op_cache_read(batch.cache, back[0].data_ptr(), back[1].data_ptr(), "bf16", s)
+        op_cache_copy([batch.K.data_ptr(), batch.V.data_ptr()], cache_page_bytes(fmt, 2, 64), pool.n_pages, [src],
+                      [free], s)
+    rng = np.random.default_rng(0)
+    for lens in ([70, 33, 64], [69, 20, 32], [1, 33, 64]):
+        batch.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        rows = rng.standard_normal((2, 3, 2, 64)).astype(np.float32)
+        k.copy_(torch.from_numpy(rows[0].reshape(3, 128)))
+        v.copy_(torch.from_numpy(rows[1].reshape(3, 128)))
+        held = [[], []]
+        for b, n in enumerate(lens):
+            pool.k[b][n - 1:n] = pool.put(0, b, n - 1, rows[0, b:b + 1])
+            pool.v[b][n - 1:n] = pool.put(1, b, n - 1, rows[1, b:b + 1])
+            held[0].append(pool.k[b][n - 1])
+            held[1].append(pool.v[b][n - 1])
+        g.replay()
+        check(batch, q, out, 8, "f32", 40, 3)
+        want = torch.from_numpy(np.stack([np.stack(h) for h in held])).float().to(torch.bfloat16)
+        assert torch.equal(back.cpu(), want.reshape(2, 3, 128))
+        assert torch.equal(batch.K[free], batch.K[src]) and torch.equal(batch.V[free], batch.V[src])
+
+
+def test_append_of_negative_zeros_and_ties_stores_what_the_definition_says():
+    """-0, values on the borders between two codes, and a block whose scale rounds to 0 beside a large one."""
+    pool = Pool("nvfp4", 1, 64, [8], seed=0)
+    batch = Batch(pool, [8])
+    x = np.zeros((8, 64), np.float32)
+    edges = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0], np.float32)
+    x[0, :8], x[0, 8:16] = edges, -edges
+    x[1] = -0.0
+    x[1, 5] = 1.0
+    x[2, 0], x[2, 16] = 1e30, 1e20
+    x[3] = np.float32(1e-38)
+    x[4, ::2] = np.nextafter(np.repeat(edges, 4), np.float32(9))[:32]
+    x[4, 1::2] = np.nextafter(np.repeat(edges, 4), np.float32(0))[:32]
+    x[5] = np.random.default_rng(0).integers(-12, 13, 64) / 2.0
+    x[6] = np.float32(3e38)
+    xd = torch.from_numpy(x).to(DEV)
+    op_cache_append(batch.cache, xd.data_ptr(), xd.data_ptr(), "f32")
+    pool.put(0, 0, 0, x[:, None])
+    pool.put(1, 0, 0, x[:, None])
+    assert np.array_equal(batch.K.cpu().numpy(), pool.K)
+    assert np.array_equal(batch.V.cpu().numpy(), pool.V)

@@ -129,6 +129,41 @@ def test_a_forks_draws_use_its_own_slot_and_its_repetition_window(weights):
     assert not np.array_equal(np.stack(got)[:, 0], np.stack(got)[:, 1])
 
 
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("T,P", [(50, 33), (24, 24), (33, 33), (96, 64)])
+def test_forks_with_caches_of_other_lengths(weights, paged, T, P):
+    """Slabs that 32 rows do not divide, and a sequence whose cache is full."""
+    d = TINY.replace(max_seq_len=T)
+    dec = decoder(weights, paged, dims=d, slots=3)
+    prompt = make_prompt(d, P, seed=P)[0]
+    dec.prefill_seq(0, prompt)
+    dec.decode_frame()
+    dec.fork_seq(0, 2)
+    for _ in range(min(4, T - P)):
+        f, z = dec.decode_frame(logits=True)
+        assert np.array_equal(z[0].view(np.uint32), z[2].view(np.uint32)) and (f[1] == -1).all()
+    if T - P < 4:
+        with pytest.raises(TfError, match="CAPACITY"):
+            dec.decode_frame()
+    dec.close()
+
+
+def test_a_fork_of_a_lockstep_batch_of_one(weights):
+    """After tf_prefill the one sequence runs on the batch-1 kernels, and with its fork on the batched ones."""
+    dec = decoder(weights, True)
+    dec.prefill(make_prompt(TINY, 11, seed=2))
+    dec.decode_frame()
+    dec.fork_seq(0, 3)
+    for _ in range(3):
+        f, z = dec.decode_frame(logits=True)
+        assert f.shape == (4, 10) and (f[1:3] == -1).all()
+        assert np.array_equal(f[0], f[3]) and np.array_equal(z[0].view(np.uint32), z[3].view(np.uint32))
+    dec.release_seq(0)
+    f, _ = dec.decode_frame()
+    assert (f[:3] == -1).all() and (f[3] >= 0).all()
+    dec.close()
+
+
 def test_fork_errors(weights):
     dec = decoder(weights, True, slots=2)
     dec.prefill_seq(0, make_prompt(TINY, 4)[0])
