@@ -109,35 +109,31 @@ class Pool:
                 head[PAGE * (D // 2 + D // 16):].view(np.float32)[r] = s[i, g]
         return held
 
-    def hidden_pages(self, b):
-        return []
-
 
 def attention(q, k, v, n, window=0, sinks=0, scale=None, hidden=None):
     """q float64 [r, Hq, D], the last r of n positions; k, v float64 [n, Hkv, D] -> out, sum p|v| (the same shape),
     per (row, head) the largest scale * sum |q||k| over what the row sees, and the largest p_j max|v_j|."""
     r, Hq, D = q.shape
-    Hkv = k.shape[1]
+    G = Hq // k.shape[1]
     scale = scale or D ** -0.5
     out, mass, reach, peak = np.zeros_like(q), np.zeros_like(q), np.zeros((r, Hq)), np.zeros((r, Hq))
-    for i in range(r):
-        p = n - r + i
-        j = np.arange(n)
-        see = j <= p
-        if window:
-            see &= (j > p - window) | (j < sinks)
-        if hidden is not None:
-            see &= ~hidden
-        if not see.any():
-            continue
-        for h in range(Hq):
-            g = h // (Hq // Hkv)
-            z = (k[see, g] @ q[i, h]) * scale
-            w = np.exp(z - z.max())
-            w /= w.sum()
-            out[i, h], mass[i, h] = w @ v[see, g], w @ np.abs(v[see, g])
-            reach[i, h] = (np.abs(k[see, g]) @ np.abs(q[i, h])).max() * scale
-            peak[i, h] = (w * np.abs(v[see, g]).max(-1)).max()
+    p, j = np.arange(n - r, n)[:, None], np.arange(n)[None]
+    see = j <= p
+    if window:
+        see &= (j > p - window) | (j < sinks)
+    if hidden is not None:
+        see &= ~hidden
+    rows = see.any(1)
+    used = see.any(0)                       # what no row sees may be anything
+    for h in range(Hq):
+        kg, vg = (np.where(used[:, None], x[:n, h // G], 0.0) for x in (k, v))
+        z = np.where(see, (q[:, h] @ kg.T) * scale, -np.inf)
+        top = np.where(rows, z.max(1, initial=-np.inf), 0.0)
+        w = np.exp(z - top[:, None])
+        w /= np.where(rows, w.sum(1), 1.0)[:, None]
+        out[:, h], mass[:, h] = w @ vg, w @ np.abs(vg)
+        reach[:, h] = np.where(see, np.abs(q[:, h]) @ np.abs(kg).T, 0.0).max(1, initial=0.0) * scale
+        peak[:, h] = (w * np.abs(vg).max(1, initial=0.0)[None]).max(1, initial=0.0)
     return out, mass, reach, peak
 
 
