@@ -17,11 +17,10 @@ __device__ __forceinline__ void cache_flag(const CacheBatch& c, uint32_t bits) {
 struct SeqRows {
   int r0, n, len;
 };
-__device__ __forceinline__ SeqRows cache_seq(const CacheBatch& c, int b) {
+__device__ __forceinline__ SeqRows cache_rows(const CacheBatch& c, int r0, int r1, int len) {
   SeqRows s;
-  s.r0 = c.row_start ? __ldg(c.row_start + b) : b;
-  const int r1 = c.row_start ? __ldg(c.row_start + b + 1) : b + 1;
-  s.len = __ldg(c.len + b);
+  s.r0 = r0;
+  s.len = len;
   s.n = 0;
   if (s.r0 < 0 || r1 < s.r0 || r1 > c.n_rows || r1 - s.r0 > c.max_rows) {
     cache_flag(c, TF_CACHE_BAD_ROWS);
@@ -31,6 +30,11 @@ __device__ __forceinline__ SeqRows cache_seq(const CacheBatch& c, int b) {
     s.n = r1 - s.r0;
   }
   return s;
+}
+
+__device__ __forceinline__ SeqRows cache_seq(const CacheBatch& c, int b) {
+  return cache_rows(c, c.row_start ? __ldg(c.row_start + b) : b, c.row_start ? __ldg(c.row_start + b + 1) : b + 1,
+                    __ldg(c.len + b));
 }
 
 // Page of block-table entry i of sequence b, or -1 (flagged) outside the pool.

@@ -248,10 +248,15 @@ __global__ void __launch_bounds__(32 * W, DecCfg<D, FMT, NT, F32, W>::kPerSm)
   // Ragged batches of more CTAs than fit at once: the longest sequences first, so that the last CTAs to
   // start are short ones.
   int b = blockIdx.z;
+  SeqRows sq;
   if (sorted) {
-    __shared__ int lens[kSortMax], chosen;
+    __shared__ int lens[kSortMax], starts[kSortMax + 1], chosen;
     const int n = c.n_seq;
-    for (int t = threadIdx.x; t < n; t += C::kThreads) lens[t] = __ldg(c.len + t);
+    for (int t = threadIdx.x; t < n; t += C::kThreads) {
+      lens[t] = __ldg(c.len + t);
+      starts[t] = c.row_start ? __ldg(c.row_start + t) : t;
+    }
+    if (threadIdx.x == 0) starts[n] = c.row_start ? __ldg(c.row_start + n) : n;
     __syncthreads();
     for (int t = threadIdx.x; t < n; t += C::kThreads) {
       int r = 0;
@@ -261,8 +266,10 @@ __global__ void __launch_bounds__(32 * W, DecCfg<D, FMT, NT, F32, W>::kPerSm)
     }
     __syncthreads();
     b = chosen;
+    sq = cache_rows(c, starts[b], starts[b + 1], lens[b]);
+  } else {
+    sq = cache_seq(c, b);
   }
-  const SeqRows sq = cache_seq(c, b);
   const int c0 = tile * C::kCols;
   const int ncol = min(C::kCols, sq.n * G - c0);
   if (ncol <= 0) return;  // the whole cluster
@@ -295,7 +302,21 @@ __global__ void __launch_bounds__(32 * W, DecCfg<D, FMT, NT, F32, W>::kPerSm)
   }
   __syncwarp();
 
-  // the queries' loads go out first: they are used after the stages have been asked for
+  // ---- this warp's stages: gw, gw + nw, ...
+  const int gw = rank * C::kWarps + warp, nw = csize * C::kWarps;
+  const int mine = gw < units ? (units - gw + nw - 1) / nw : 0;
+  auto unit_at = [&](int i) {
+    const int u = gw + i * nw;
+    return u < usink ? u : ulow + u - usink;
+  };
+  // page ids of up to 32 stages ahead, one per lane
+  int ids = -1;
+  auto look_up = [&](int from) {
+    const int i = from + lane;
+    ids = i < mine ? cache_page(c, b, unit_at(i) / (kKvPage / C::kKeys)) : -1;
+  };
+  look_up(0);
+  // the queries' loads go out behind the table's; they are used after the stages have been asked for
   constexpr int QC = C::kCols / C::kWarps;  // columns a warp prepares: warp, warp + kWarps, ...
   float xq[QC][D / 32];                     // dims lane, lane + 32, ...
 #pragma unroll
@@ -310,21 +331,8 @@ __global__ void __launch_bounds__(32 * W, DecCfg<D, FMT, NT, F32, W>::kPerSm)
       }
     }
   }
-  // ---- this warp's stages: gw, gw + nw, ...
-  const int gw = rank * C::kWarps + warp, nw = csize * C::kWarps;
-  const int mine = gw < units ? (units - gw + nw - 1) / nw : 0;
-  auto unit_at = [&](int i) {
-    const int u = gw + i * nw;
-    return u < usink ? u : ulow + u - usink;
-  };
-  // page ids of up to 32 stages ahead, one per lane
-  int ids = -1;
-  auto look_up = [&](int from) {
-    const int i = from + lane;
-    ids = i < mine ? cache_page(c, b, unit_at(i) / (kKvPage / C::kKeys)) : -1;
-  };
   auto issue = [&](int i) {  // all lanes; stage i of this warp into ring slot i % kStages
-    if ((i & 31) == 0) look_up(i);
+    if (i && (i & 31) == 0) look_up(i);
     const int page = __shfl_sync(0xFFFFFFFFu, ids, i & 31);
     if (lane == 0) {
       const int s = i % C::kStages;
@@ -558,7 +566,7 @@ __global__ void __launch_bounds__(32 * W, DecCfg<D, FMT, NT, F32, W>::kPerSm)
       // false, and nothing changed: a reference has to be replaced first (asked only where `checked`)
       auto weights = [&](auto mask_, bool checked) -> bool {
         constexpr bool kMask = decltype(mask_)::value;
-        bool again = unset;
+        bool again = false;
         uint64_t sum2[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -653,9 +661,10 @@ __global__ void __launch_bounds__(32 * W, DecCfg<D, FMT, NT, F32, W>::kPerSm)
       // FMT 1: each weight's f16 parts are off by 2^-23 of it (two parts) or by 2^-25, half of f16's smallest step,
       // i.e. 2^-32 of the largest weight.
       auto soft = [&](auto mask_) {
-        for (int turn = 0; turn < 2; ++turn) {
-          if (weights(mask_, turn == 0)) break;
+        const bool start = __any_sync(0xFFFFFFFFu, unset);  // no reference yet: nothing to try first
+        if (start || !weights(mask_, true)) {
           replace_refs();
+          weights(mask_, false);
         }
       };
       if (whole)
