@@ -29,9 +29,9 @@
 //     of the rows that see it.
 // Measured (GB300, 32 query and 8 KV heads of 128): a tile of 128 keys takes a CTA
 // about 3200 cycles with bf16 pages (the four products; 2600 at the measured dense
-// rate) and 5000 with 4-bit pages (the softmax behind the products: its scales and
+// rate) and 4800 with 4-bit pages (the softmax behind the products: its scales and
 // the converters' instructions).  Four ragged chunks of up to 1024 rows, window 1024:
-// 73 us (53 GFLOP); 2 x 1024 rows over 5120 4-bit positions: 200 us (155 GFLOP).
+// 73 us (53 GFLOP); 2 x 1024 rows over 5120 4-bit positions: 193 us (155 GFLOP).
 // Every wait is bounded; the TMEM columns are always released.
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -72,7 +72,7 @@ struct PromptCfg {
   static constexpr int kThreads = FMT ? 32 * 16 : 32 * 12;
   static constexpr int kMmaWarp = FMT ? 12 : 8;
   // Quarters of a tile whose p a lane keeps before it stores them: what its registers hold (FMT 1, 2 x 1024 rows
-  // over 5120 positions: 219 us with 1, 199 with 2, 204 with 4, which spills).
+  // over 5120 positions: 193 us with 2, 206 with 4, which spills).
   static constexpr int kGroup = FMT ? 2 : 4;
   static constexpr uint32_t kCols = 512;
   // kind::f16, fp32 accumulate, bf16 operands, M = 128.  S: B = K tile, K-major, N = 128.
@@ -777,19 +777,14 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
           load(q, s);
           if constexpr (kKind > 0) masks(q, see);
           if constexpr (kKind == 2) poison = in->poison[q] >> (2 * lt);
-          float2 kss[4], vss[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            kss[i] = vss[i] = make_float2(p.scale_log2, p.scale_log2);
-            if constexpr (FMT == 1) {
-              kss[i] = *reinterpret_cast<const float2*>(in->ks + q * 32 + 8 * i + 2 * lt);
-              vss[i] = *reinterpret_cast<const float2*>(in->vs + q * 32 + 8 * i + 2 * lt);
-            }
-          }
           tm_wait_ld(s);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float2 ks = kss[i], vs = vss[i];
+            float2 ks = make_float2(p.scale_log2, p.scale_log2), vs = ks;
+            if constexpr (FMT == 1) {  // (read where they are used: 193 us of the case above, 199 ahead of the wait)
+              ks = *reinterpret_cast<const float2*>(in->ks + q * 32 + 8 * i + 2 * lt);
+              vs = *reinterpret_cast<const float2*>(in->vs + q * 32 + 8 * i + 2 * lt);
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t* sr = &s[k >> 1][4 * i + 2 * (k & 1)];
