@@ -474,8 +474,9 @@ tf_status tf_op_gemv(const void* W, int32_t dtype, const float* row_scale,
  *   of one head) is quantised as tf_op_quantize_nvfp4 does a weight row,
  *   except that the scale of a row of zeros is 0: s = amax / 2688, b =
  *   e4m3(min(amax of 16 / (6 s), 448)), code = e2m1(clamp(x / (b s), -6, 6)),
- *   each step one float32 operation; the value is e2m1 * b * s.  A row with an
- *   infinity or a NaN gets the row scale NaN (and zero codes).
+ *   each step one float32 operation; the value is e2m1 * b * s (the sign of a
+ *   zero is not specified).  A row with an infinity or a NaN gets the row scale
+ *   NaN (and zero codes).
  *   K pool: codes [32][D/2], the even element in the low nibble; block scales
  *     [32][D/16].
  *   V pool, with position 8t + 2j + i of the page (t < 4, j < 4, i < 2): codes
@@ -547,8 +548,9 @@ tf_status tf_op_attention_cache(const tf_kv_cache* cache, const void* q, int64_t
 /* Writes the sequences' rows k, v ([n_rows] rows of n_kv_heads*D elements,
  * `stride` elements apart, 0: n_kv_heads*D) to their positions in the pools,
  * rounded to bfloat16 or quantised; rows at negative positions are skipped.
- * Two sequences of a call must not name the same page for positions that both
- * write.  Errors: TF_E_INVAL, TF_E_CUDA. */
+ * No two sequences of a call, and no two calls at a time, may write into the
+ * same page (two positions of a 4-bit V page share their bytes).
+ * Errors: TF_E_INVAL, TF_E_CUDA. */
 tf_status tf_op_cache_append(const tf_kv_cache* cache, const void* k, const void* v, int64_t stride,
                              int32_t dtype, void* stream);
 
