@@ -389,7 +389,9 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
       // ---------------------------------------------------------------- MMA issuer
       if (lane == 0) {
         bool ok = true;
-        if (boxed) {  // pairs are consecutive (row, head) rows of Q: one box per tile and 64 columns
+        // pairs are consecutive (row, head) rows of Q: one box per tile and 64 columns (none where no row sees a key:
+        // nothing would wait for them)
+        if (boxed && nt > 0) {
           mbar_arrive_expect_tx(q_full, NX * C::kTile);
 #pragma unroll
           for (int x = 0; x < NX; ++x)
@@ -679,7 +681,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
     auto from_lane = [&](int64_t v, int src) {
       return static_cast<int64_t>(__shfl_sync(0xFFFFFFFFu, static_cast<long long>(v), src));
     };
-    if (!boxed) {
+    if (!boxed && nt > 0) {
       const int64_t at = pair_at(lane / kLines * (8 * kLines) + warp * kLines + lane % kLines, p.q_stride);
 #pragma unroll 4
       for (int it = 0; it < kChunks; ++it) {
@@ -698,7 +700,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
         }
       }
     }
-    if (!boxed) {
+    if (!boxed && nt > 0) {
       asm volatile("cp.async.wait_all;" ::: "memory");
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(q_full);

@@ -177,3 +177,22 @@ def test_one_call_after_another_and_side_by_side(fmt):
     batch.lens.copy_(torch.tensor([450, 270], dtype=torch.int32))
     g.replay()
     check(batch, q, outs[0], 32, "bf16", 100, 5)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("Hkv,ratio,D,pad", [(8, 4, 128, 0), (8, 4, 64, 0), (8, 3, 64, 0), (8, 4, 64, 1)])
+def test_many_rows_at_negative_positions(fmt, Hkv, ratio, D, pad):
+    """Whole tiles of rows before position 0, among others: zeros, whatever the queries hold, and nothing of them is
+    left behind for the tiles that follow."""
+    lens, counts = [600, 20, 0, 400], [300, 500, 200, 400]
+    batch = Batch(pool_of(fmt, Hkv, D, lens), counts)
+    q = queries(batch, Hkv * ratio, "bf16", 8, pad=pad)
+    q[300:780] = float("nan")                            # the 480 rows of the second sequence, the 200 of the third
+    q[800:1000] = float("nan")
+    outs = [attend(batch, q, Hkv * ratio, "bf16", pad=pad) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    assert (outs[0][300:780, :Hkv * ratio * D] == 0).all() and (outs[0][800:1000, :Hkv * ratio * D] == 0).all()
+    q[300:780] = 1.0                                     # (the oracle takes finite queries)
+    q[800:1000] = 1.0
+    check(batch, q, outs[0], Hkv * ratio, "bf16")
