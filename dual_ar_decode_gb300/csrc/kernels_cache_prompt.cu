@@ -31,7 +31,7 @@
 // about 3200 cycles with bf16 pages (the four products; 2600 at the measured dense
 // rate) and 4800 with 4-bit pages (the softmax behind the products: its scales and
 // the converters' instructions).  Four ragged chunks of up to 1024 rows, window 1024:
-// 73 us (53 GFLOP); 2 x 1024 rows over 5120 4-bit positions: 193 us (155 GFLOP).
+// 74 us (53 GFLOP); 2 x 1024 rows over 5120 4-bit positions: 193 us (155 GFLOP).
 // Every wait is bounded; the TMEM columns are always released.
 #include <cuda.h>
 #include <cuda_fp16.h>
