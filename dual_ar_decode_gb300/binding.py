@@ -396,6 +396,5 @@ def op_cache_copy(pools, page_bytes, n_pages, src, dst, stream=0):
     dst = np.ascontiguousarray(dst, dtype=np.int32)
     if src.shape != dst.shape or src.ndim != 1:
         raise ValueError("src and dst are lists of the same length")
-    _check(lib().tf_op_cache_copy(bases.buffer_info()[0], len(bases), page_bytes, n_pages,
-                                  src.__array_interface__["data"][0], dst.__array_interface__["data"][0],
-                                  src.size, stream))
+    _check(lib().tf_op_cache_copy(bases.buffer_info()[0], len(bases), page_bytes, n_pages, src.tobytes(),
+                                  dst.tobytes(), src.size, stream))
