@@ -147,6 +147,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{.reg .pred q; elect.sync _|q, 0xFFFFFFFF; selp.u32 %0, 1, 0, q;}" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
@@ -386,67 +392,73 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
   if (warp >= 8) {
     if constexpr (FMT == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     if (warp == C::kMmaWarp) {
-      // ---------------------------------------------------------------- MMA issuer
-      if (lane == 0) {
-        bool ok = true;
-        // pairs are consecutive (row, head) rows of Q: one box per tile and 64 columns (none where no row sees a key:
-        // nothing would wait for them)
-        if (boxed && nt > 0) {
-          mbar_arrive_expect_tx(q_full, NX * C::kTile);
+      // ---------------------------------------------------------------- MMA issuer: the warp stays together, one
+      // lane issues (a loop that only one lane runs computes every operand in its own registers and moves it to the
+      // warp's: the tensor core waits for it)
+      bool ok = true;
+      // pairs are consecutive (row, head) rows of Q: one box per tile and 64 columns (none where no row sees a key:
+      // nothing would wait for them)
+      if (boxed && nt > 0 && elect_one()) {
+        mbar_arrive_expect_tx(q_full, NX * C::kTile);
 #pragma unroll
-          for (int x = 0; x < NX; ++x)
+        for (int x = 0; x < NX; ++x)
 #pragma unroll
-            for (int h = 0; h < D / 64; ++h)
-              tma_box3(smem_u32(smem) + x * C::kTile + h * 16384, &map_q, h * 64, hkv * G,
-                       sq.r0 + (c0 + x * 128) / G, q_full);
+          for (int h = 0; h < D / 64; ++h)
+            tma_box3(smem_u32(smem) + x * C::kTile + h * 16384, &map_q, h * 64, hkv * G,
+                     sq.r0 + (c0 + x * 128) / G, q_full);
+      }
+      auto score = [&](int x, int j) {  // S_x = Q_x K(j)^T
+        const uint64_t qd = desc_k(smem_u32(smem) + x * C::kTile), kd = desc_k(smem_u32(sk) + (j & 1) * C::kTile);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+          mma_ss(tmem + x * 128, qd + off, kd + off, C::kIdescS, kk > 0 ? 1u : 0u);
         }
-        auto score = [&](int x, int j) {  // S_x = Q_x K(j)^T
-          const uint32_t qb = smem_u32(smem) + x * C::kTile, kb = smem_u32(sk) + (j & 1) * C::kTile;
+        mma_commit(&s_full[x]);
+      };
+      if (nt > 0) {
+        ok = bar_wait_warp(q_full, 0) && bar_wait_warp(&k_full[0], 0);
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        if (ok && elect_one()) {
+          score(0, 0);
+          if constexpr (NX > 1) score(1, 0);
+          mma_commit(&k_empty[0]);
+        }
+      }
+      for (int j = 0; ok && j < nt; ++j) {
+        const uint64_t vd = desc_mn(smem_u32(sv) + (j & 1) * C::kTile);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-            mma_ss(tmem + x * 128, desc_k(qb + off), desc_k(kb + off), C::kIdescS, kk > 0 ? 1u : 0u);
-          }
-          mma_commit(&s_full[x]);
-        };
-        if (nt > 0) {
-          ok = bar_wait(q_full, 0) && bar_wait(&k_full[0], 0);
+        for (int x = 0; x < NX; ++x) {
+          ok = ok && bar_wait_warp(&p_full[x], j & 1) &&
+               (x || bar_wait_warp(FMT ? &v_full[j & 1] : &v_clean[j & 1], (j >> 1) & 1));
+          if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          if (ok) {
-            score(0, 0);
-            if constexpr (NX > 1) score(1, 0);
-            mma_commit(&k_empty[0]);
-          }
-        }
-        for (int j = 0; ok && j < nt; ++j) {
-#pragma unroll
-          for (int x = 0; x < NX; ++x) {
-            ok = ok && bar_wait(&p_full[x], j & 1) && (x || bar_wait(FMT ? &v_full[j & 1] : &v_clean[j & 1], (j >> 1) & 1));
-            if (!ok) break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint32_t vb = smem_u32(sv) + (j & 1) * C::kTile;
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              mma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, desc_mn(vb + kk * 2048), C::kIdescO,
+              mma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, vd + (kk * 2048 >> 4), C::kIdescO,
                      (j > 0 || kk > 0) ? 1u : 0u);
             if (x == NX - 1) mma_commit(&v_empty[j & 1]);
-            if (j + 1 < nt) {
-              if (!x) {
-                ok = bar_wait(&k_full[(j + 1) & 1], ((j + 1) >> 1) & 1);
-                if (!ok) break;
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-              }
+            if (j + 1 == nt) mma_commit(&o_done[x]);
+          }
+          __syncwarp();
+          if (j + 1 < nt) {
+            if (!x) {
+              ok = bar_wait_warp(&k_full[(j + 1) & 1], ((j + 1) >> 1) & 1);
+              if (!ok) break;
+              asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            }
+            if (elect_one()) {
               score(x, j + 1);  // after the product that reads P_x, in issue order; its commit covers both
               if (x == NX - 1) mma_commit(&k_empty[(j + 1) & 1]);
-            } else {
-              mma_commit(&o_done[x]);
             }
+            __syncwarp();
           }
         }
-        if (!ok) *failed = 1;
-        mma_commit(drained);  // nothing may be in flight when the columns are released
-        if (!bar_wait(drained, 0)) *failed = 1;
       }
+      if (!ok && lane == 0) *failed = 1;
+      if (elect_one()) mma_commit(drained);  // nothing may be in flight when the columns are released
+      if (!bar_wait_warp(drained, 0) && lane == 0) *failed = 1;
     } else {
       if constexpr (FMT == 0) {
         // -------------------------------------------------------------- TMA producer
