@@ -326,7 +326,9 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
   volatile uint32_t* failed = tmem_slot + 1;
 
   const CacheBatch& c = p.c;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the shuffle, and the reduction below: values that the compiler knows to be the warp's, as the tensor core takes
+  // its addresses; 184 us of the 4-bit case above without them, 174 with them)
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int hkv = blockIdx.y, b = blockIdx.z;
   const int G = p.Hq / c.Hkv;
   const SeqRows sq = cache_seq(c, b);
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
       mbar_init(&k_full[i], FMT ? 128 : 1);
       mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], FMT ? 128 : 1);
-      mbar_init(&v_clean[i], 64);
+      mbar_init(&v_clean[i], 2);
       mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 128);
@@ -385,7 +387,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __reduce_or_sync(0xFFFFFFFFu, *tmem_slot);
 
   // FMT 1: the softmax's warpgroups take registers from the other two: 256 x 160 + 256 x 96 = the launch's
   // 512 x 128
@@ -429,8 +431,9 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
         const uint64_t vd = desc_mn(smem_u32(sv) + (j & 1) * C::kTile);
 #pragma unroll
         for (int x = 0; x < NX; ++x) {
-          ok = ok && bar_wait_warp(&p_full[x], j & 1) &&
-               (x || bar_wait_warp(FMT ? &v_full[j & 1] : &v_clean[j & 1], (j >> 1) & 1));
+          // (P last: the others are there as a rule, and nothing then lies between P and its product)
+          ok = ok && (x || bar_wait_warp(FMT ? &v_full[j & 1] : &v_clean[j & 1], (j >> 1) & 1)) &&
+               bar_wait_warp(&p_full[x], j & 1);
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           if (elect_one()) {
@@ -532,7 +535,8 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
                 for (int ch = 0; ch < D / 8; ++ch) *chunk_at(vt, r, ch) = make_uint4(0u, 0u, 0u, 0u);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            mbar_arrive(&v_clean[j & 1]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&v_clean[j & 1]);
           }
         }
       } else if (warp < 12) {
