@@ -33,7 +33,7 @@
 //     they grow past a bound, which one vote per page finds: in the steady state a
 //     page needs no shuffles.
 // Measured (GB300, 32 query and 8 KV heads of 128): 32 ragged 4-bit streams of up to
-// 32768 positions, bf16 rows, 106 us (5.9 TB/s; 563 warp instructions per head
+// 32768 positions, bf16 rows, 100 us (6.3 TB/s; 563 warp instructions per head
 // page, issue slots and HBM are both near their end); 32 bf16 streams with a
 // window of 2048, float32 rows, 41 us (5.6 TB/s); 32 x 8192 bf16 positions 163 us
 // (6.6 TB/s, memory); one 4-bit sequence of 4096 positions 8.2 us (latency).
@@ -241,7 +241,10 @@ __global__ void __launch_bounds__(32 * W, DecCfg<D, FMT, NT, F32, W>::kPerSm)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const CacheBatch& c = p.c;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = lane >> 2, lt = lane & 3;
+  // (the shuffle: a value that the compiler knows to be the warp's, so what follows from it takes no registers of the
+  // lanes'; 32 ragged 4-bit streams 106 us without it, 100 with it)
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int lg = lane >> 2, lt = lane & 3;
   const int rank = static_cast<int>(blockIdx.x) % csize, tile = static_cast<int>(blockIdx.x) / csize;
   const int hkv = blockIdx.y;
   const int G = p.Hq / c.Hkv;
@@ -997,7 +1000,7 @@ float cache_decode_us(const CacheAttnParams& p) {
   const DecPlan d = decode_plan(p, nt, p.c.fmt ? kKvPage : kKvPage / 2, warps);
   const int slots = (p.c.fmt ? 16 : 8) / warps * 152;
   const int64_t waves = (d.groups * d.cs + slots - 1) / slots;
-  const float stage = p.c.fmt ? (p.c.D == 128 ? 2.05f : 1.15f) : (p.c.D == 128 ? 1.3f : 1.05f);
+  const float stage = p.c.fmt ? (p.c.D == 128 ? 1.92f : 1.08f) : (p.c.D == 128 ? 1.3f : 1.05f);
   return static_cast<float>(waves) * ((p.c.fmt ? 6.f : 5.f) + stage * static_cast<float>((d.units + warps * d.cs - 1) / (warps * d.cs)));
 }
 

@@ -28,10 +28,10 @@
 //     or a NaN that only some rows see is zeroed too and made a NaN probability
 //     of the rows that see it.
 // Measured (GB300, 32 query and 8 KV heads of 128): a tile of 128 keys takes a CTA
-// about 3200 cycles with bf16 pages (the four products; 2600 at the measured dense
-// rate) and 4800 with 4-bit pages (the softmax behind the products: its scales and
+// about 3000 cycles with bf16 pages (the four products; 2600 at the measured dense
+// rate) and 4000 with 4-bit pages (the softmax behind the products: its scales and
 // the converters' instructions).  Four ragged chunks of up to 1024 rows, window 1024:
-// 74 us (53 GFLOP); 2 x 1024 rows over 5120 4-bit positions: 193 us (155 GFLOP).
+// 67 us (53 GFLOP); 2 x 1024 rows over 5120 4-bit positions: 170 us (155 GFLOP).
 // Every wait is bounded; the TMEM columns are always released.
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -72,7 +72,7 @@ struct PromptCfg {
   static constexpr int kThreads = FMT ? 32 * 16 : 32 * 12;
   static constexpr int kMmaWarp = FMT ? 12 : 8;
   // Quarters of a tile whose p a lane keeps before it stores them: what its registers hold (FMT 1, 2 x 1024 rows
-  // over 5120 positions: 193 us with 2, 206 with 4, which spills).
+  // over 5120 positions: 170 us with 2, 184 with 1; 4 spills).
   static constexpr int kGroup = FMT ? 2 : 4;
   static constexpr uint32_t kCols = 512;
   // kind::f16, fp32 accumulate, bf16 operands, M = 128.  S: B = K tile, K-major, N = 128.
@@ -799,7 +799,7 @@ __global__ void __launch_bounds__(PromptCfg<D, FMT>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float2 ks = make_float2(p.scale_log2, p.scale_log2), vs = ks;
-            if constexpr (FMT == 1) {  // (read where they are used: 193 us of the case above, 199 ahead of the wait)
+            if constexpr (FMT == 1) {  // (read where they are used: 3% of the case above against ahead of the wait)
               ks = *reinterpret_cast<const float2*>(in->ks + q * 32 + 8 * i + 2 * lt);
               vs = *reinterpret_cast<const float2*>(in->vs + q * 32 + 8 * i + 2 * lt);
             }
@@ -1020,8 +1020,8 @@ int64_t prompt_ctas(const CacheAttnParams& p, int span) {
   const int64_t each = ((int64_t)p.c.max_rows * G + span - 1) / span * p.c.n_seq;
   return std::min(each, p.c.n_rows * G / span + p.c.n_seq) * p.c.Hkv;
 }
-// Pairs of a CTA: 128 while that still is one wave of CTAs (a tile of keys takes 1.48 us with one 128-pair tile and
-// 1.63 with two, bf16, D = 128, so two pay once the CTAs queue).
+// Pairs of a CTA: 128 while that still is one wave of CTAs (a tile of keys takes 1.40 us with one 128-pair tile and
+// 1.54 with two, bf16, D = 128, so two pay once the CTAs queue).
 int prompt_span(const CacheAttnParams& p) { return prompt_ctas(p, 128) <= 152 ? 128 : 256; }
 
 // Rows of queries or outputs as boxes of 64 columns x G heads x `rows` rows.
@@ -1066,15 +1066,15 @@ cudaError_t launch_prompt_t(const CUtensorMap& mk, const CUtensorMap& mv, const 
 
 }  // namespace
 
-// Measured with rows that see everything (4-bit and bf16 pages, D = 64 and 128, 1 and 8 sequences, 512 and 4096
-// positions): start and end of a CTA, and a tile of 128 keys.
+// Measured with rows that see everything (4-bit and bf16 pages, D = 64 and 128, 512 and 1024 rows, 512 and 4608
+// positions before them): start and end of a CTA, and a tile of 128 keys.
 float cache_prompt_us(const CacheAttnParams& p) {
   const int span = prompt_span(p);
   const int64_t waves = (prompt_ctas(p, span) + 151) / 152;
   const int64_t rows = std::max<int64_t>(1, span / (p.Hq / p.c.Hkv));
   const int64_t keys = p.window > 0 ? std::min<int64_t>(p.c.max_len, (int64_t)p.window + p.sinks + rows + 64) : p.c.max_len;
-  const float start = p.c.fmt ? (p.c.D == 128 ? 8.5f : 7.0f) : (p.c.D == 128 ? 7.5f : 6.3f);
-  const float tile = (p.c.fmt ? (p.c.D == 128 ? 2.3f : 2.0f) : (p.c.D == 128 ? 1.63f : 1.43f)) * (span == 128 ? 0.91f : 1.f);
+  const float start = p.c.fmt ? (p.c.D == 128 ? 7.5f : 6.0f) : (p.c.D == 128 ? 7.0f : 6.4f);
+  const float tile = (p.c.fmt ? (p.c.D == 128 ? 2.07f : 1.92f) : (p.c.D == 128 ? 1.54f : 1.23f)) * (span == 128 ? 0.91f : 1.f);
   return static_cast<float>(waves) * (start + tile * static_cast<float>((keys + 127) / 128));
 }
 
