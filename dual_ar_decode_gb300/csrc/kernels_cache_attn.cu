@@ -33,9 +33,9 @@
 //     they grow past a bound, which one vote per page finds: in the steady state a
 //     page needs no shuffles.
 // Measured (GB300, 32 query and 8 KV heads of 128): 32 ragged 4-bit streams of up to
-// 32768 positions, bf16 rows, 100 us (6.3 TB/s; 563 warp instructions per head
+// 32768 positions, bf16 rows, 100 us (6.3 TB/s; 530 warp instructions per head
 // page, issue slots and HBM are both near their end); 32 bf16 streams with a
-// window of 2048, float32 rows, 41 us (5.6 TB/s); 32 x 8192 bf16 positions 163 us
+// window of 2048, float32 rows, 40 us (5.7 TB/s); 32 x 8192 bf16 positions 163 us
 // (6.6 TB/s, memory); one 4-bit sequence of 4096 positions 8.2 us (latency).
 #include <cuda.h>
 #include <cuda_fp16.h>
